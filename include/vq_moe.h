@@ -300,6 +300,143 @@ vq_status vq_fit(const uint16_t *w, int32_t rows, int32_t cols, int32_t d, int32
                  int32_t n_sample, const int32_t *init, int32_t iters, uint16_t *scales, uint16_t *codebook,
                  uint16_t *codes, void *workspace, size_t ws_bytes, void *stream);
 
+/* ---- The block around the experts ----
+ * A MoE block is more than its routed experts: a norm makes x from the residual stream, the router's load has to
+ * stay balanced when it is trained, dense 4-bit projections (a shared expert) run beside the experts, and the
+ * block's output is normed, gated, scaled and added back. The calls below are those row-wise and dense parts. They
+ * follow the conventions above; T = 0 launches nothing and returns VQ_OK (row pointers may then be NULL). */
+
+/* A root-mean-square norm over rows of `hidden` elements: n(v)[c] = v[c] * rsqrt(mean(v^2) + eps) * (weight[c] +
+ * weight_offset). weight: device [hidden] of weight_dtype (VQ_F32 or VQ_BF16); weight_offset is 1 for checkpoints
+ * that store weight - 1, else 0. eps >= 0, finite. Sums of squares are fp32: a row whose sum of squares leaves
+ * fp32's range gives what fp32 arithmetic gives (0 or NaN). An Inf or NaN stays in its own row. */
+typedef struct vq_norm {
+    int32_t hidden;
+    int32_t weight_dtype;
+    const void *weight;
+    float eps;
+    float weight_offset;
+} vq_norm;
+
+/* Row arrays of the norm calls: a device pointer, an element type (VQ_F32 or VQ_BF16) where both are taken, and
+ * `ld`, the elements from one row to the next (>= hidden; any value when T = 1). Pointers are aligned to their
+ * element; rows on 16-byte boundaries (pointers, and ld * element size) with hidden a multiple of 8 take the
+ * vector kernels, others the scalar ones (same results up to the order of the row sums). hidden is 1 to 16384
+ * (VQ_ERR_UNSUPPORTED beyond). Outputs must not overlap inputs unless said. Gradients of bf16 arrays are bf16;
+ * weight gradients are fp32 [hidden]. All row arithmetic is fp32, each output rounded once. */
+
+/* The norm that makes a block's input: x[t] = bf16(n(h[t])). h: [T, hidden] of h_dtype; x: bf16 [T, hidden]. */
+vq_status vq_norm_pre(const vq_norm *n, const void *h, int32_t h_dtype, int64_t h_ld, int32_t T, uint16_t *x,
+                      int64_t x_ld, void *stream);
+
+/* Bytes of workspace the two norm backward calls need for T rows of `hidden`; 0 on invalid sizes. */
+size_t vq_norm_workspace_size(int32_t hidden, int32_t T);
+
+/* Gradient of vq_norm_pre. dx: bf16 [T, hidden]; dres: NULL, or [T, hidden] of h_dtype, a gradient that reaches h
+ * past the norm (the residual path) and is added. With r = rsqrt(mean(h^2) + eps) and g = (weight + offset) dx:
+ *   dh = r g - r^3 h mean(g h) + dres        (h_dtype; may be dres itself, same ld)
+ *   dweight = sum_t dx h r                   (fp32 [hidden], or NULL: not computed)
+ * The sum over rows runs in a fixed order: equal calls give equal bits. T = 0 writes dweight = 0. workspace:
+ * 256-byte aligned, vq_norm_workspace_size bytes; needed (VQ_ERR_WORKSPACE) only with dweight. Calls that may
+ * overlap on the GPU need workspaces of their own. */
+vq_status vq_norm_pre_backward(const vq_norm *n, const void *h, int32_t h_dtype, int64_t h_ld, const uint16_t *dx,
+                               int64_t dx_ld, const void *dres, int64_t dres_ld, int32_t T, void *dh, int64_t dh_ld,
+                               float *dweight, void *workspace, size_t ws_bytes, void *stream);
+
+/* A block's output joined to the residual stream, and the next block's norm, in one pass:
+ *   u = n_post(y[t])                                (post NULL: u = y[t])
+ *   h_out[t] = res_scale * h[t] + out_scale * sigmoid(gate[t]) * u       (gate NULL: factor 1)
+ *   x_out[t] = bf16(n_next(h_out[t]))               (next NULL: not computed; of h_out as stored)
+ * y: [T, hidden] of y_dtype (a layer's output). gate: logits of gate_dtype, gate_cols = 1 (one per token, element t *
+ * gate_ld) or gate_cols = hidden (one per channel). h and h_out: h_dtype; h_out may be h itself (same ld). post and
+ * next must have the same hidden as given. */
+vq_status vq_norm_post(const vq_norm *post, const vq_norm *next, int32_t hidden, const void *y, int32_t y_dtype,
+                       int64_t y_ld, const void *gate, int32_t gate_dtype, int32_t gate_cols, int64_t gate_ld,
+                       const void *h, int32_t h_dtype, int64_t h_ld, float res_scale, float out_scale, int32_t T,
+                       void *h_out, int64_t h_out_ld, uint16_t *x_out, int64_t x_out_ld, void *stream);
+
+/* Gradient of vq_norm_post from y, gate and the stored h_out. dh_out: [T, hidden] of h_dtype, or NULL (0): the
+ * gradient that reaches h_out past the next norm; dx_out: bf16, required with next, else NULL. With dH = dh_out +
+ * (n_next's gradient of dx_out at h_out), s = sigmoid(gate), dv = out_scale * dH:
+ *   dh = res_scale * dH                                   (h_dtype; may be dh_out itself, same ld; NULL: not wanted)
+ *   dy = n_post's gradient of s * dv at y                 (y_dtype)
+ *   dgate = s (1 - s) * dv * u, summed over the row when gate_cols = 1  (gate_dtype; NULL: not wanted)
+ *   dpost = sum_t s dv y r_post,  dnext = sum_t dx_out h_out r_next     (fp32 [hidden]; each NULL: not wanted)
+ * The rounding of h_out is taken as the identity. T = 0 writes zero weight gradients. workspace as in
+ * vq_norm_pre_backward, needed only with dpost or dnext. */
+vq_status vq_norm_post_backward(const vq_norm *post, const vq_norm *next, int32_t hidden, const void *y,
+                                int32_t y_dtype, int64_t y_ld, const void *gate, int32_t gate_dtype, int32_t gate_cols,
+                                int64_t gate_ld, const void *h_out, int32_t h_dtype, int64_t h_out_ld, float res_scale,
+                                float out_scale, int32_t T, const void *dh_out, int64_t dh_out_ld,
+                                const uint16_t *dx_out, int64_t dx_out_ld, void *dy, int64_t dy_ld, void *dgate,
+                                int64_t dgate_ld, void *dh, int64_t dh_ld, float *dpost, float *dnext, void *workspace,
+                                size_t ws_bytes, void *stream);
+
+/* Bytes of workspace vq_balance_loss needs; 0 on invalid sizes. */
+size_t vq_balance_workspace_size(int32_t T, int32_t E);
+
+/* The router's balance loss and the experts' load, over the tokens that count (mask NULL, or mask[t] != 0; mask:
+ * device bytes [T]). logits: device fp32 [T, E], ids: device int32 [T, top_k], both as vq_route takes and gives
+ * them; an id outside [0, E) is a dropped pair and is not counted, an id twice in a token counts twice.
+ *   counts[e] = pairs routed to e, e < E;  counts[E] = V, the tokens that count       (int32 [E + 1])
+ *   probs[e]  = (1 / V) sum_t softmax(logits[t])[e]                                   (fp32 [E]; 0 when V = 0)
+ *   loss      = coef * sum_e (E counts[e] / (V top_k)) probs[e]                       (fp32 [1])
+ * (coef when the load is even). A token whose logits are all -Inf has probability 0 everywhere; other Inf and NaN
+ * follow IEEE. Masked rows are not read. Column sums run in a fixed order: equal calls give equal bits. Limits as
+ * vq_route (E <= 4096, 1 <= top_k <= min(E, 32), T * top_k < 2^31). workspace: 256-byte aligned. T = 0 writes
+ * zeros (logits, ids and mask may then be NULL). */
+vq_status vq_balance_loss(const float *logits, const int32_t *ids, const uint8_t *mask, int32_t T, int32_t E,
+                          int32_t top_k, float coef, float *loss, int32_t *counts, float *probs, void *workspace,
+                          size_t ws_bytes, void *stream);
+
+/* Gradient of vq_balance_loss at the logits, the counts held fixed. counts: as written by vq_balance_loss for the
+ * same mask; dloss: device fp32 [1], or NULL for 1.  With d[e] = E counts[e] / (V top_k):
+ *   dlogits[t, e] = dloss * coef / V * p[t, e] * (d[e] - sum_e' p[t, e'] d[e'])     (fp32 [T, E])
+ * Masked tokens, and all tokens when V = 0, get 0. dlogits may be logits itself. */
+vq_status vq_balance_loss_backward(const float *logits, const int32_t *counts, const uint8_t *mask, int32_t T,
+                                   int32_t E, int32_t top_k, float coef, const float *dloss, float *dlogits,
+                                   void *stream);
+
+/* A dense matrix of 4-bit integers with group scales, W [rows, cols]:
+ *   W[r, c] = fp32(scale[r, c / group]) * (q[r, c] - 8)                                  without biases
+ *   W[r, c] = fp32(scale[r, c / group]) * q[r, c] + fp32(bias[r, c / group])             with biases
+ * group is 32, 64 or 128 and divides cols; rows and cols are 1 to 2^30. (The d = 1, 4-bit modules above look their values up in a
+ * codebook and have groups of 64 only.) words, scales and biases are in the tile layout that vq_q4_pack writes. */
+typedef struct vq_q4_module {
+    int32_t rows;
+    int32_t cols;
+    int32_t group;
+    const uint32_t *words;     /* device, 16-byte aligned: vq_q4_packed_words(rows, cols) words */
+    const uint16_t *scales;    /* device, 16-byte aligned: fp16, vq_q4_packed_scales(rows, cols, group) */
+    const uint16_t *biases;    /* device, 16-byte aligned, or NULL: as scales */
+} vq_q4_module;
+
+/* Words, and fp16 scales (or biases), of a packed module: 16-row by 128-column tiles, the last ones padded with
+ * codes, scales and biases of 0. 0 on invalid arguments. */
+size_t vq_q4_packed_words(int32_t rows, int32_t cols);
+size_t vq_q4_packed_scales(int32_t rows, int32_t cols, int32_t group);
+
+/* Lays a module out for vq_q4_gemv, once, when it is loaded. codes: device uint32 [rows, cols / 8], row-major, code c
+ * in bits 4 (c % 8) of word c / 8 (vq_pack's layout for 4 bits); scales, biases: device fp16 [rows, cols / group],
+ * row-major, biases and biases_out NULL together. Outputs: device, 16-byte aligned, of the sizes above.
+ * Tile (i, j) (rows 16 i, columns 128 j; j fastest) is 256 words: word ((b * 32) + l) * 4 + s, lane l = 4 g + c,
+ * holds rows 16 i + g and 16 i + g + 8, columns k .. k + 3 with k = 128 j + 64 b + 32 (s / 2) + 8 c + 4 (s % 2): in
+ * bits 4 m and 16 + 4 m the codes of row g + 8 (m % 2), columns k + 2 (m / 2) and k + 2 (m / 2) + 1. A tile's scales
+ * are [8 (g)][128 / group][2 (rows g, g + 8)]. */
+vq_status vq_q4_pack(const uint32_t *codes, const uint16_t *scales, const uint16_t *biases, int32_t rows, int32_t cols,
+                     int32_t group, uint32_t *words_out, uint16_t *scales_out, uint16_t *biases_out, void *stream);
+
+/* Matrix-vector products of T tokens with a packed 4-bit module (the dense, codebook-free sibling of vq_gemv):
+ *   m1 NULL:  y[t, r] = sum_c W0[r, c] x[t, c]
+ *   else:     y[t, r] = silu(sum_c W0[r, c] x[t, c]) * sum_c W1[r, c] x[t, c]      (a gate and up pair)
+ * m1 has m0's rows, cols and group, and biases when m0 has them. x: device bf16 [T, cols], row stride x_ld >= cols
+ * elements, 16-byte aligned, x_ld a multiple of 8 (T > 1). y: device [T, rows] of y_dtype, row stride y_ld >= rows,
+ * aligned to its element. x enters the tensor cores unrounded as bf16 against the exact integers q - 8; group sums,
+ * scales and the sum over groups are fp32 in a fixed order, and y is rounded once. The weights are streamed once for
+ * every 32 tokens: the call is meant for decode-sized T. */
+vq_status vq_q4_gemv(const vq_q4_module *m0, const vq_q4_module *m1, const uint16_t *x, int64_t x_ld, int32_t T,
+                     void *y, int32_t y_dtype, int64_t y_ld, void *stream);
+
 /* Diagnostic (synchronises `stream`). Every wait of the library's pipelined
  * kernels on an on-chip barrier is bounded; a kernel that gives up records a
  * nonzero word at offset 0 of the MoE workspace it ran with (the routing

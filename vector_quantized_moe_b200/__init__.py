@@ -10,6 +10,7 @@ Names follow include/vq_moe.h.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional
@@ -44,13 +45,24 @@ class vq_moe_layer(ctypes.Structure):
     _fields_ = [("gate", vq_module), ("up", vq_module), ("down", vq_module)]
 
 
+class vq_norm(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
+class vq_q4_module(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("words", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("biases", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m vector_quantized_moe_b200.build`")
     lib = ctypes.CDLL(LIB_PATH)
-    P, I32, SZ, I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int64
+    P, I32, SZ, I64, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int64, ctypes.c_float
     MP = ctypes.POINTER(vq_module)
     LP = ctypes.POINTER(vq_moe_layer)
+    NP, QP = ctypes.POINTER(vq_norm), ctypes.POINTER(vq_q4_module)
     sig = {
         "vq_status_str": (ctypes.c_char_p, [ctypes.c_int]),
         "vq_geometry_supported": (ctypes.c_int, [I32, I32]),
@@ -72,6 +84,20 @@ def _load():
         "vq_set_wait_limit": (ctypes.c_int, [I64]),
         "vq_moe_check": (ctypes.c_int, [P, P]),
         "vq_moe_decode_noalloc": (ctypes.c_int, [LP, P, I32, P, I32, I32, P, I32, P]),
+        "vq_norm_pre": (ctypes.c_int, [NP, P, I32, I64, I32, P, I64, P]),
+        "vq_norm_workspace_size": (SZ, [I32, I32]),
+        "vq_norm_pre_backward": (ctypes.c_int, [NP, P, I32, I64, P, I64, P, I64, I32, P, I64, P, P, SZ, P]),
+        "vq_norm_post": (ctypes.c_int, [NP, NP, I32, P, I32, I64, P, I32, I32, I64, P, I32, I64, F, F, I32, P, I64, P,
+                                        I64, P]),
+        "vq_norm_post_backward": (ctypes.c_int, [NP, NP, I32, P, I32, I64, P, I32, I32, I64, P, I32, I64, F, F, I32, P,
+                                                 I64, P, I64, P, I64, P, I64, P, I64, P, P, P, SZ, P]),
+        "vq_balance_workspace_size": (SZ, [I32, I32]),
+        "vq_balance_loss": (ctypes.c_int, [P, P, P, I32, I32, I32, F, P, P, P, P, SZ, P]),
+        "vq_balance_loss_backward": (ctypes.c_int, [P, P, P, I32, I32, I32, F, P, P, P]),
+        "vq_q4_packed_words": (SZ, [I32, I32]),
+        "vq_q4_packed_scales": (SZ, [I32, I32, I32]),
+        "vq_q4_pack": (ctypes.c_int, [P, P, P, I32, I32, I32, P, P, P, P]),
+        "vq_q4_gemv": (ctypes.c_int, [QP, QP, P, I64, I32, P, I32, I64, P]),
         "vq_fit_workspace_size": (SZ, [I32, I32]),
         "vq_fit": (ctypes.c_int, [P, I32, I32, I32, I32, P, I32, P, I32, P, P, P, P, SZ, P]),
     }
@@ -299,6 +325,346 @@ def fit_check(workspace, stream=None) -> int:
     """Status of the error word of a vq_fit workspace returned by fit() (vq_moe_check)."""
     base = (workspace.data_ptr() + 255) // 256 * 256
     return int(_L().vq_moe_check(base, _stream(stream)))
+
+
+# ------------------------------------------------------------------ the block around the experts
+#
+# norm -> (router) -> experts and 4-bit shared expert -> gate, norm, residual, next norm, and the router's balance
+# loss. bf16 arrays may be torch.bfloat16 or their int16 bit patterns; outputs are torch.bfloat16. Rows may be
+# windows of wider arrays (a row stride), with consecutive elements inside a row. Every call checks its tensors
+# (VQError with VQ_ERR_ARG) before it launches, runs on its tensors' device, and on `stream` when one is given (the
+# outputs then belong to that stream).
+
+def _device_call(f):
+    """Runs f on the device of its tensors and on the `stream` argument, if any."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        torch = _torch()
+        if stream is None:
+            dev = _device_of((*args, *kw.values()) if kw else args)
+            if dev is None or dev == torch._C._cuda_getDevice():
+                return f(*args, **kw)
+            with torch.cuda.device(dev):
+                return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            out = f(*args, **kw)
+        for t in (*args, *kw.values()):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
+        return out
+    return call
+
+
+def _device_of(args):
+    """CUDA device index of the first tensor (or weight) among args; None when that is not on a GPU."""
+    Tensor = _torch().Tensor
+    for a in args:
+        if isinstance(a, Tensor):
+            return a.get_device() if a.is_cuda else None
+    return None
+
+
+def _raw_stream(dev: int) -> int:
+    return _torch()._C._cuda_getCurrentRawStream(dev)
+
+
+def _bad(where: str):
+    raise VQError(VQ_ERR_ARG, where)
+
+
+_dtype_codes = None
+
+
+def _dtype_code(dtype):
+    """VQ_F32 or VQ_BF16 of a tensor type, None for any other."""
+    global _dtype_codes
+    if _dtype_codes is None:
+        torch = _torch()
+        _dtype_codes = {torch.float32: VQ_F32, torch.bfloat16: VQ_BF16, torch.int16: VQ_BF16}
+    return _dtype_codes.get(dtype)
+
+
+def _row_arg(where, t, T, cols, like=None):
+    """(pointer, dtype, row stride) of a [T, cols] array; VQError when t is not one. like: its required dtype code."""
+    if t is None:
+        return None, VQ_F32, 0
+    code = _dtype_code(t.dtype)
+    if code is None or (like is not None and code != like) or t.dim() != 2:
+        _bad(where)
+    shape, stride = t.shape, t.stride()
+    if shape[0] != T or shape[1] != cols or (cols > 1 and stride[1] != 1) or (T > 1 and stride[0] < cols):
+        _bad(where)
+    return t.data_ptr(), code, stride[0]
+
+
+def _same_device(where, *tensors) -> int:
+    """Index of the one GPU that all tensors (None: skipped) are on, which is the current device."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0 or (dev >= 0 and d != dev):
+                _bad(where + " (tensors on different devices, or not on a GPU)")
+            dev = d
+    if dev != _torch()._C._cuda_getDevice():
+        _bad(where + " (stream of another device)")
+    return dev
+
+
+def _empty_ws(n, workspace, dev):
+    """(tensor, aligned pointer, bytes) of a workspace of n bytes: the given one, or a new one."""
+    ws = workspace if workspace is not None else _torch().empty(n + 256, dtype=_torch().uint8, device=dev)
+    base = ws.data_ptr()
+    aligned = (base + 255) // 256 * 256
+    return ws, aligned, ws.numel() * ws.element_size() - (aligned - base)
+
+
+class Norm:
+    """The weight of a root-mean-square norm (vq_norm): weight [hidden] fp32 or bf16; offset is 1 for checkpoints that
+    store weight - 1."""
+
+    def __init__(self, weight, eps: float = 1e-6, offset: float = 0.0):
+        code = _dtype_code(weight.dtype)
+        if code is None or weight.dim() != 1 or weight.numel() < 1 or not weight.is_contiguous():
+            _bad("Norm: weight")
+        self.weight, self.hidden = weight, weight.numel()
+        self._s = vq_norm(self.hidden, code, weight.data_ptr(), eps, offset)
+        self._ref = ctypes.byref(self._s)
+
+
+@_device_call
+def norm_pre(norm: Norm, h, out=None):
+    """x [T, hidden] bf16 = norm(h), the input of a block from the residual stream h (fp32 or bf16) (vq_norm_pre)."""
+    T, H = h.shape[0], norm.hidden
+    hp, hd, hl = _row_arg("norm_pre: h", h, T, H)
+    if out is None:
+        out = _torch().empty((T, H), dtype=_torch().bfloat16, device=h.device)
+    xp, _, xl = _row_arg("norm_pre: out", out, T, H, VQ_BF16)
+    dev = _same_device("norm_pre", h, norm.weight, out)
+    _check(_L().vq_norm_pre(norm._ref, hp, hd, hl, T, xp, xl, _raw_stream(dev)), "vq_norm_pre")
+    return out
+
+
+@functools.lru_cache(maxsize=None)
+def _norm_ws(H, T):
+    return int(_L().vq_norm_workspace_size(H, T))
+
+
+@_device_call
+def norm_pre_backward(norm: Norm, h, dx, dres=None, weight_grad: bool = True, workspace=None):
+    """(dh, dweight fp32 or None) of norm_pre for the gradient dx (bf16); dres: a gradient that reaches h past the
+    norm, added to dh (vq_norm_pre_backward)."""
+    torch = _torch()
+    T, H = h.shape[0], norm.hidden
+    hp, hd, hl = _row_arg("norm_pre_backward: h", h, T, H)
+    xp, _, xl = _row_arg("norm_pre_backward: dx", dx, T, H, VQ_BF16)
+    rp, _, rl = _row_arg("norm_pre_backward: dres", dres, T, H, hd)
+    dh = torch.empty((T, H), dtype=torch.float32 if hd == VQ_F32 else torch.bfloat16, device=h.device)
+    dev = _same_device("norm_pre_backward", h, norm.weight, dx, dres, workspace)
+    dw = wp = None
+    nb = 0
+    if weight_grad:
+        dw = torch.empty(H, dtype=torch.float32, device=h.device)
+        workspace, wp, nb = _empty_ws(_norm_ws(H, T), workspace, h.device)
+    _check(_L().vq_norm_pre_backward(norm._ref, hp, hd, hl, xp, xl, rp, rl, T, dh.data_ptr(), H, _ptr(dw), wp, nb,
+                                     _raw_stream(dev)), "vq_norm_pre_backward")
+    return dh, dw
+
+
+def _gate_arg(where, gate, T, H):
+    """(pointer, dtype, columns, row stride) of gate logits [T], [T, 1] or [T, H]."""
+    if gate is None:
+        return None, VQ_F32, 0, 0
+    cols = 1 if gate.dim() == 1 else gate.shape[1] if gate.dim() == 2 else 0
+    if cols != 1 and cols != H:
+        _bad(where)
+    p, d, ld = _row_arg(where, gate.unsqueeze(1) if gate.dim() == 1 else gate, T, cols)
+    return p, d, cols, ld
+
+
+def _norm_ref(where, norm, H):
+    if norm is None:
+        return None
+    if norm.hidden != H:
+        _bad(where)
+    return norm._ref
+
+
+@_device_call
+def norm_post(y, h, post: Optional[Norm] = None, gate=None, res_scale: float = 1.0, out_scale: float = 1.0,
+              next: Optional[Norm] = None, h_out=None, x_out=None):
+    """(h_out, x_out) of a block whose output is y [T, hidden] and whose residual stream is h:
+    h_out = res_scale * h + out_scale * sigmoid(gate) * post(y) and x_out = next(h_out) in bf16 (None without next).
+    gate: logits [T], [T, 1] or [T, hidden]. h_out may be h (vq_norm_post)."""
+    torch = _torch()
+    T, H = y.shape if y.dim() == 2 else _bad("norm_post: y")
+    yp, yd, yl = _row_arg("norm_post: y", y, T, H)
+    hp, hd, hl = _row_arg("norm_post: h", h, T, H)
+    gp, gd, gc, gl = _gate_arg("norm_post: gate", gate, T, H)
+    pr, nr = _norm_ref("norm_post: post", post, H), _norm_ref("norm_post: next", next, H)
+    if x_out is not None and next is None:
+        _bad("norm_post: x_out without next")
+    if h_out is None:
+        h_out = torch.empty((T, H), dtype=torch.float32 if hd == VQ_F32 else torch.bfloat16, device=y.device)
+    if x_out is None and next is not None:
+        x_out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
+    op, _, ol = _row_arg("norm_post: h_out", h_out, T, H, hd)
+    xp, _, xl = _row_arg("norm_post: x_out", x_out, T, H, VQ_BF16)
+    dev = _same_device("norm_post", y, h, gate, h_out, x_out, None if post is None else post.weight,
+                       None if next is None else next.weight)
+    _check(_L().vq_norm_post(pr, nr, H, yp, yd, yl, gp, gd, gc, gl, hp, hd, hl, res_scale, out_scale, T, op, ol, xp, xl,
+                             _raw_stream(dev)), "vq_norm_post")
+    return h_out, x_out
+
+
+@_device_call
+def norm_post_backward(y, h_out, dh_out, dx_out=None, post: Optional[Norm] = None, gate=None, res_scale: float = 1.0,
+                       out_scale: float = 1.0, next: Optional[Norm] = None, workspace=None):
+    """(dy, dgate, dh, dpost, dnext) of norm_post from its y, gate and h_out and the gradients dh_out (may be None: 0)
+    and dx_out (with next). Gradients of bf16 arrays are bf16, dpost and dnext fp32; None for what the call did not
+    have (vq_norm_post_backward)."""
+    torch = _torch()
+    T, H = y.shape if y.dim() == 2 else _bad("norm_post_backward: y")
+    yp, yd, yl = _row_arg("norm_post_backward: y", y, T, H)
+    hp, hd, hl = _row_arg("norm_post_backward: h_out", h_out, T, H)
+    gp, gd, gc, gl = _gate_arg("norm_post_backward: gate", gate, T, H)
+    ap, _, al = _row_arg("norm_post_backward: dh_out", dh_out, T, H, hd)
+    xp, _, xl = _row_arg("norm_post_backward: dx_out", dx_out, T, H, VQ_BF16)
+    pr = _norm_ref("norm_post_backward: post", post, H)
+    nr = _norm_ref("norm_post_backward: next", next, H)
+    if (dx_out is None) != (next is None):
+        _bad("norm_post_backward: dx_out goes with next")
+    dev = _same_device("norm_post_backward", y, h_out, gate, dh_out, dx_out, workspace,
+                       None if post is None else post.weight, None if next is None else next.weight)
+    like = lambda code: torch.float32 if code == VQ_F32 else torch.bfloat16  # noqa: E731
+    dy = torch.empty((T, H), dtype=like(yd), device=y.device)
+    dh = torch.empty((T, H), dtype=like(hd), device=y.device)
+    dgate = None if gate is None else torch.empty(gate.shape, dtype=like(gd), device=y.device)
+    dpost = None if post is None else torch.empty(H, dtype=torch.float32, device=y.device)
+    dnext = None if next is None else torch.empty(H, dtype=torch.float32, device=y.device)
+    wp, nb = None, 0
+    if post is not None or next is not None:
+        workspace, wp, nb = _empty_ws(_norm_ws(H, T), workspace, y.device)
+    _check(_L().vq_norm_post_backward(pr, nr, H, yp, yd, yl, gp, gd, gc, gl, hp, hd, hl, res_scale, out_scale, T, ap, al,
+                                      xp, xl, dy.data_ptr(), H, _ptr(dgate), gc, dh.data_ptr(), H, _ptr(dpost),
+                                      _ptr(dnext), wp, nb, _raw_stream(dev)), "vq_norm_post_backward")
+    return dy, dgate, dh, dpost, dnext
+
+
+def _mask_arg(where, mask, T):
+    if mask is None:
+        return None
+    if mask.dtype not in (_torch().bool, _torch().uint8) or mask.dim() != 1 or mask.shape[0] != T or \
+            not mask.is_contiguous():
+        _bad(where)
+    return mask.data_ptr()
+
+
+def _logits_arg(where, logits):
+    if logits.dtype != _torch().float32 or logits.dim() != 2 or not logits.is_contiguous():
+        _bad(where)
+    return logits.shape
+
+
+@functools.lru_cache(maxsize=None)
+def _balance_ws(T, E):
+    return int(_L().vq_balance_workspace_size(T, E))
+
+
+@_device_call
+def balance_loss(logits, ids, mask=None, coef: float = 1.0, workspace=None):
+    """(loss fp32 scalar, counts int32 [E + 1], probs fp32 [E]) of router logits [T, E] (fp32) and the ids [T, k]
+    that route() chose: counts[e] pairs go to expert e, counts[E] tokens count (mask, bool or bytes [T], leaves others
+    out), probs is the mean softmax, loss = coef * sum_e (E counts[e] / (counts[E] k)) probs[e] (vq_balance_loss)."""
+    torch = _torch()
+    T, E = _logits_arg("balance_loss: logits", logits)
+    if ids.dtype != torch.int32 or ids.dim() != 2 or ids.shape[0] != T or not ids.is_contiguous():
+        _bad("balance_loss: ids")
+    mp = _mask_arg("balance_loss: mask", mask, T)
+    dev = _same_device("balance_loss", logits, ids, mask, workspace)
+    loss = torch.empty((), dtype=torch.float32, device=logits.device)
+    counts = torch.empty(E + 1, dtype=torch.int32, device=logits.device)
+    probs = torch.empty(E, dtype=torch.float32, device=logits.device)
+    workspace, wp, nb = _empty_ws(_balance_ws(T, E), workspace, logits.device)
+    _check(_L().vq_balance_loss(logits.data_ptr(), ids.data_ptr(), mp, T, E, ids.shape[1], coef, loss.data_ptr(),
+                                counts.data_ptr(), probs.data_ptr(), wp, nb, _raw_stream(dev)), "vq_balance_loss")
+    return loss, counts, probs
+
+
+@_device_call
+def balance_loss_backward(logits, counts, top_k: int, dloss=None, mask=None, coef: float = 1.0):
+    """dlogits fp32 [T, E] of balance_loss, from the counts it gave for the same mask; dloss: fp32 scalar tensor on
+    the device, None for 1 (vq_balance_loss_backward)."""
+    torch = _torch()
+    T, E = _logits_arg("balance_loss_backward: logits", logits)
+    if counts.dtype != torch.int32 or counts.dim() != 1 or counts.shape[0] != E + 1 or not counts.is_contiguous():
+        _bad("balance_loss_backward: counts")
+    if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != 1):
+        _bad("balance_loss_backward: dloss")
+    mp = _mask_arg("balance_loss_backward: mask", mask, T)
+    dev = _same_device("balance_loss_backward", logits, counts, mask, dloss)
+    out = torch.empty((T, E), dtype=torch.float32, device=logits.device)
+    _check(_L().vq_balance_loss_backward(logits.data_ptr(), counts.data_ptr(), mp, T, E, top_k, coef, _ptr(dloss),
+                                         out.data_ptr(), _raw_stream(dev)), "vq_balance_loss_backward")
+    return out
+
+
+class Q4Module:
+    """A dense 4-bit matrix [rows, cols] with group scales on the device, in the kernel's tile layout (vq_q4_module)."""
+
+    def __init__(self, rows, cols, group, words, scales, biases=None):
+        self.rows, self.cols, self.group = rows, cols, group
+        self.words, self.scales, self.biases = words, scales, biases
+        self._s = vq_q4_module(rows, cols, group, _ptr(words), _ptr(scales), _ptr(biases))
+        self._ref = ctypes.byref(self._s)
+
+    @classmethod
+    def from_rows(cls, words, scales, biases=None, group: int = 64, stream=None):
+        """Lays row-major device arrays out (vq_q4_pack): words int32 [rows, cols / 8] (pack(codes, 4)'s rows), scales
+        and biases fp16 (or their int16 bits) [rows, cols / group]. Without biases W = scale * (q - 8), with them
+        W = scale * q + bias."""
+        return _q4_from_rows(words, scales, biases, group, stream=stream)
+
+
+@_device_call
+def _q4_from_rows(words, scales, biases, group):
+    torch = _torch()
+    if words.dtype not in (torch.int32, torch.uint32) or words.dim() != 2 or not words.is_contiguous():
+        _bad("Q4Module.from_rows: words")
+    rows, cols = words.shape[0], words.shape[1] * 8
+    if group not in (32, 64, 128) or cols % group:
+        _bad("Q4Module.from_rows: group")
+    for name, t in (("scales", scales), ("biases", biases)):
+        if t is not None and (t.dtype not in (torch.float16, torch.int16) or tuple(t.shape) != (rows, cols // group)
+                              or not t.is_contiguous()):
+            _bad("Q4Module.from_rows: " + name)
+    nw, ns = int(_L().vq_q4_packed_words(rows, cols)), int(_L().vq_q4_packed_scales(rows, cols, group))
+    if nw == 0 or ns == 0:
+        _bad("Q4Module.from_rows")
+    dev = _same_device("Q4Module.from_rows", words, scales, biases)
+    w = torch.empty(nw, dtype=torch.int32, device=words.device)
+    s = torch.empty(ns, dtype=torch.int16, device=words.device)
+    b = None if biases is None else torch.empty(ns, dtype=torch.int16, device=words.device)
+    _check(_L().vq_q4_pack(words.data_ptr(), scales.data_ptr(), _ptr(biases), rows, cols, group, w.data_ptr(),
+                           s.data_ptr(), _ptr(b), _raw_stream(dev)), "vq_q4_pack")
+    return Q4Module(rows, cols, group, w, s, b)
+
+
+@_device_call
+def q4_gemv(m: Q4Module, x, up: Optional[Q4Module] = None, out_dtype=None, out=None):
+    """y [T, rows] = x [T, cols] (bf16) . W^T; with up: silu(x . W^T) * (x . W_up^T) (vq_q4_gemv). out_dtype: float32
+    or bfloat16 (the default, or out's)."""
+    torch = _torch()
+    T = x.shape[0]
+    xp, _, xl = _row_arg("q4_gemv: x", x, T, m.cols, VQ_BF16)
+    if out is None:
+        out = torch.empty((T, m.rows), dtype=out_dtype or torch.bfloat16, device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        _bad("q4_gemv: out_dtype")
+    yp, yd, yl = _row_arg("q4_gemv: out", out, T, m.rows)
+    dev = _same_device("q4_gemv", x, m.words, None if up is None else up.words, out)
+    _check(_L().vq_q4_gemv(m._ref, None if up is None else up._ref, xp, xl, T, yp, yd, yl, _raw_stream(dev)), "vq_q4_gemv")
+    return out
 
 
 def set_trace_events(events) -> None:

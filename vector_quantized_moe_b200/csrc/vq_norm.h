@@ -1,0 +1,80 @@
+// Arguments of the block-norm kernels (vq_norm.cu, vq_norm_bwd.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "vq_internal.h"
+
+namespace vq {
+
+constexpr int NORM_MAX_HIDDEN = 16384;
+
+// A norm's parameters; weight NULL: no norm.
+struct NormDev {
+    const void *weight;
+    int dtype;
+    float eps, offset;
+};
+
+enum { GATE_NONE = 0, GATE_TOKEN = 1, GATE_CHANNEL = 2 };
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+#endif
+
+struct NormPreArgs {
+    NormDev n;
+    const void *h;
+    uint16_t *x;
+    int64_t h_ld, x_ld;
+    int T, H, W;          // W: warps per row
+    float inv_h;          // 1 / H
+};
+
+struct NormPostArgs {
+    NormDev post, next;
+    const void *y, *gate, *h;
+    void *h_out;
+    uint16_t *x;
+    int64_t y_ld, gate_ld, h_ld, ho_ld, x_ld;
+    int gate_mode, gate_dtype;
+    int T, H, W;
+    float inv_h, res_scale, out_scale;
+};
+
+struct NormPreBwdArgs {
+    NormDev n;
+    const void *h, *dres;      // dres NULL: none
+    const uint16_t *dx;
+    void *dh;
+    int64_t h_ld, dx_ld, dres_ld, dh_ld;
+    float *part;               // [parts][H] partial weight gradients; NULL: not wanted
+    int T, H, W;
+    float inv_h;
+};
+
+struct NormPostBwdArgs {
+    NormDev post, next;
+    const void *y, *gate, *h, *dho;   // dho NULL: zero
+    const uint16_t *dx;
+    void *dy, *dgate, *dh;            // dgate, dh NULL: not wanted
+    int64_t y_ld, gate_ld, h_ld, dho_ld, dx_ld, dy_ld, dgate_ld, dh_ld;
+    float *part1, *part2;             // [parts][H] each; NULL: not wanted
+    int gate_mode, gate_dtype;
+    int T, H, W;
+    float inv_h, res_scale, out_scale;
+};
+
+// vec8: every row (pointers and strides) on 16-byte boundaries and H a multiple of 8.
+cudaError_t launch_norm_pre(const NormPreArgs &a, int h_dtype, bool vec8, cudaStream_t s);
+cudaError_t launch_norm_post(const NormPostArgs &a, int y_dtype, int h_dtype, bool vec8, cudaStream_t s);
+
+// The backward launches sum the weight gradients over the rows in `ws`
+// (norm_workspace_bytes) and finish them in d1 / d2 (each may be NULL).
+size_t norm_workspace_bytes(int H, int T);
+cudaError_t launch_norm_pre_bwd(const NormPreBwdArgs &a, int h_dtype, bool vec8, float *dw, float *ws, cudaStream_t s);
+cudaError_t launch_norm_post_bwd(const NormPostBwdArgs &a, int y_dtype, int h_dtype, bool vec8, float *dpost,
+                                 float *dnext, float *ws, cudaStream_t s);
+
+}  // namespace vq
