@@ -420,8 +420,9 @@ size_t vq_q4_packed_scales(int32_t rows, int32_t cols, int32_t group);
  * in bits 4 (c % 8) of word c / 8 (vq_pack's layout for 4 bits); scales, biases: device fp16 [rows, cols / group],
  * row-major, biases and biases_out NULL together. Outputs: device, 16-byte aligned, of the sizes above.
  * Tile (i, j) (rows 16 i, columns 128 j; j fastest) is 256 words: word ((b * 32) + l) * 4 + s, lane l = 4 g + c,
- * holds rows 16 i + g and 16 i + g + 8, columns k .. k + 3 with k = 128 j + 64 b + 32 (s / 2) + 8 c + 4 (s % 2): in
- * bits 4 m and 16 + 4 m the codes of row g + 8 (m % 2), columns k + 2 (m / 2) and k + 2 (m / 2) + 1. A tile's scales
+ * holds rows 16 i + g and 16 i + g + 8, columns k .. k + 3 with k = 128 j + 64 b + 32 (s / 2) + 8 c + 4 (s % 2): rotated
+ * right by 4 m bits (m = 0 .. 3), it has the codes of row g + 8 (m % 2), columns k + 2 (m / 2) and k + 2 (m / 2) + 1 in
+ * bits 3 to 6 and 19 to 22. A tile's scales
  * are [8 (g)][128 / group][2 (rows g, g + 8)]. */
 vq_status vq_q4_pack(const uint32_t *codes, const uint16_t *scales, const uint16_t *biases, int32_t rows, int32_t cols,
                      int32_t group, uint32_t *words_out, uint16_t *scales_out, uint16_t *biases_out, void *stream);
@@ -431,8 +432,9 @@ vq_status vq_q4_pack(const uint32_t *codes, const uint16_t *scales, const uint16
  *   else:     y[t, r] = silu(sum_c W0[r, c] x[t, c]) * sum_c W1[r, c] x[t, c]      (a gate and up pair)
  * m1 has m0's rows, cols and group, and biases when m0 has them. x: device bf16 [T, cols], row stride x_ld >= cols
  * elements, 16-byte aligned, x_ld a multiple of 8 (T > 1). y: device [T, rows] of y_dtype, row stride y_ld >= rows,
- * aligned to its element. x enters the tensor cores unrounded as bf16 against the exact integers q - 8; group sums,
- * scales and the sum over groups are fp32 in a fixed order, and y is rounded once. The weights are streamed once for
+ * aligned to its element. x enters the tensor cores unrounded as bf16 against the exact integers 16 + q; group sums
+ * (24 sum x is taken off them), scales and the sum over groups are fp32 in a fixed order, and y is rounded once: the
+ * error is a few 2^-24 of sum |scale| (16 + q) |x|, which has to stay in fp32's range. The weights are streamed once for
  * every 32 tokens: the call is meant for decode-sized T. */
 vq_status vq_q4_gemv(const vq_q4_module *m0, const vq_q4_module *m1, const uint16_t *x, int64_t x_ld, int32_t T,
                      void *y, int32_t y_dtype, int64_t y_ld, void *stream);

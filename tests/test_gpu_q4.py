@@ -111,8 +111,9 @@ def test_layout_follows_its_documentation():
                         want = 0
                         for e in range(4):
                             r = 16 * i + g + 8 * (e % 2)
-                            want |= code(r, k + 2 * (e // 2)) << (4 * e)
-                            want |= code(r, k + 2 * (e // 2) + 1) << (16 + 4 * e)
+                            both = code(r, k + 2 * (e // 2)) | code(r, k + 2 * (e // 2) + 1) << 16
+                            n = 3 + 4 * e   # rotated left
+                            want |= (both << n | both >> (32 - n)) & 0xFFFFFFFF
                         assert out[(i * nsb + j) * 256 + (b * 32 + lane) * 4 + p] == want
             for g in range(8):
                 for grp in range(ng):

@@ -386,8 +386,9 @@ cudaError_t fwd(const BalanceArgs &a, int ctas, int per_cta, int one, cudaStream
 {
     const size_t smem = balance_smem(a.E);
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(vq_balance_kernel<PER, VEC>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static std::atomic<uint64_t> allowed{0};
+        const int most = PER > 0 ? (BAL_WARPS * BAL_REG_E + BAL_REG_E + 1) * 4 : (BAL_WIDE_WARPS * 4096 + 4097) * 4;
+        const cudaError_t e = allow_smem((const void *)vq_balance_kernel<PER, VEC>, most, allowed);
         if (e != cudaSuccess)
             return e;
     }

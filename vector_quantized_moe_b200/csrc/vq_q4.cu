@@ -1,17 +1,21 @@
 // Dense 4-bit matrix-vector products with group scales.
 //
 //   y[t, r] = sum_g ( s[r, g] sum_{c in g} (q[r, c] - 8) x[t, c]  +  (b[r, g] + 8 s[r, g]) sum_{c in g} x[t, c] )
-// (the second term with biases only). The integers q - 8 are exact in bf16, so
-// the inner sums run on the tensor cores (mma m16n8k16: 16 rows of W against 8
+// (the second term with biases only). The integers are exact in bf16, so the
+// inner sums run on the tensor cores (mma m16n8k16: 16 rows of W against 8
 // tokens) with x unrounded and fp32 accumulators; scales and the sum over
-// groups are fp32. A group's sum of x comes out of the same instruction
-// against a row of ones, in the lanes that need it.
+// groups are fp32. What the tensor cores get is 16 + q: a code moved into the
+// upper mantissa bits of 16.0 needs one shift and one mask-or per pair of
+// weights and no subtraction. 24 times a group's sum of x comes off its sum in
+// fp32; the sum of x comes out of the same instruction against ones, in the
+// lanes that need it. The offset makes the sums of a group about 5 times
+// larger than those of q - 8, so their fp32 rounding counts that much more
+// (measured against 64 bits: 3e-7 of the result's norm, a plain fp32 product
+// 3e-7).
 //
 // The weights dominate the bytes (0.5 byte each, read once), so the layout is
 // the lanes' own: one 16-byte load per lane is four mma A operands of a 16 x 64
-// block, a warp's load 512 contiguous bytes. A nibble pair becomes a bf16 pair
-// with one mask-or (0x4300 | q is 128 + q) and one subtraction of 136, 11
-// instructions per 8 weights.
+// block, a warp's load 512 contiguous bytes.
 //
 // A warp takes R row tiles at one column tile at a time, so that its x
 // fragments serve R tiles; the CTA's warps take column tiles in turn and add
@@ -27,39 +31,31 @@ namespace {
 
 constexpr uint32_t BF16_ONES = 0x3F803F80u;
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+// d (+)= a b, from zero when `first`.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool first)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    if (first)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+            "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+            "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The four bf16 pairs q - 8 of a packed word.
+// The four bf16 pairs 16 + q of a packed word: rotated by 4 i, code i of each
+// half sits in the upper four mantissa bits of 16.0 (0x4180).
 __device__ __forceinline__ void decode(uint32_t w, uint32_t (&a)[4])
 {
-    const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));   // 136
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t v = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), off);
-        a[i] = *reinterpret_cast<const uint32_t *>(&d);
-    }
-}
-
-// A lane's scale (or bias) pairs of a column tile: NG pairs (rows g, g + 8), 4 NG bytes.
-template <int NG>
-__device__ __forceinline__ void load_pairs(const uint16_t *p, uint32_t (&v)[NG])
-{
-    if constexpr (NG == 4) {
-        const uint4 t = ldg_u128(p);
-        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-    } else if constexpr (NG == 2) {
-        const uint2 t = ldg_u64(reinterpret_cast<const uint32_t *>(p));
-        v[0] = t.x, v[1] = t.y;
-    } else {
-        v[0] = ldg_u32(reinterpret_cast<const uint32_t *>(p));
+        const uint32_t v = i == 3 ? __funnelshift_r(w, w, 12) : w >> (4 * i);
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(a[i]) : "r"(v), "r"(0x00780078u), "r"(0x41804180u));   // v & mask | 16.0
     }
 }
 
@@ -68,37 +64,114 @@ __device__ __forceinline__ float2 half_pair(uint32_t v)
     return __half22float2(*reinterpret_cast<const __half2 *>(&v));
 }
 
-// R: row tiles per warp (of a pair: R / 2 of each module); NT: 8-token tiles.
-template <int R, int NT, int G, bool BIAS>
-__global__ void __launch_bounds__(256) vq_q4_gemv_kernel(const Q4Args a)
+// Most warps per CTA (and per row group): the kernels' registers decide.
+template <int R, int NT>
+constexpr int MAX_WARPS = R == 4 ? 4 : R == 2 && NT < 4 ? 16 : 8;
+constexpr long Q4_WANT_WARPS = 148 * 16;   // 16 warps on every SM
+
+// CTAs of that size an SM holds at least.
+template <int R, int NT>
+constexpr int MIN_CTAS = R == 4 ? 4 : NT == 4 || MAX_WARPS<R, NT> == 16 ? 1 : NT == 2 ? 2 : 3;
+
+// Bytes of one pipeline stage of a warp: R tiles' words, their scale (and bias)
+// pairs.
+template <int R, int G, bool BIAS>
+constexpr int STAGE_BYTES = R * (1024 + 32 * (128 / G) * (BIAS ? 2 : 1));
+// Stages per warp: enough bytes in flight per SM with two CTAs resident.
+template <int R>
+constexpr int STAGES = R == 4 ? 2 : R == 2 ? 4 : 6;
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
 {
-    constexpr int NG = 128 / G;           // groups per column tile
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+
+template <int NG>
+__device__ __forceinline__ void lds_pairs(uint32_t at, uint32_t (&v)[NG])
+{
+    if constexpr (NG == 4) {
+        const uint4 t = lds128(at);
+        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+    } else if constexpr (NG == 2) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at));
+    } else {
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(at));
+    }
+}
+
+// R: row tiles per warp (of a pair: R / 2 of each module); NT: 8-token tiles.
+// ks of the CTA's warps share a row group of R tiles and take its column tiles
+// in turn.
+template <int R, int NT, int G, bool BIAS>
+__global__ void __launch_bounds__(32 * MAX_WARPS<R, NT>, MIN_CTAS<R, NT>) vq_q4_gemv_kernel(const Q4Args a, int ks)
+{
+    constexpr int NG = 128 / G;           // groups of columns per column tile
     constexpr int SPANS = G / 32;         // 32-column spans per group
-    extern __shared__ float sums[];       // [warps][R * NT * 4][32]
-    grid_dep_launch();
-    grid_dep_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    constexpr int D = STAGES<R>, SB = STAGE_BYTES<R, G, BIAS>, V = R * NT * 4;
+    extern __shared__ __align__(128) unsigned char ring[];   // [warps][D][SB]; later the warps' sums [warps][V][32]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     const int t0 = blockIdx.y * (8 * NT);
-    const int per = a.pair ? R / 2 : R;   // row tiles of a module per CTA
+    const int per = a.pair ? R / 2 : R;   // row tiles of a module per row group
+    const int kw = warp & (ks - 1);
+    const int grp = blockIdx.x * (blockDim.x / 32 / ks) + warp / ks;
+
+    // a lane's place in its row group's tiles; tiles past the last repeat it (their sums are not stored)
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring) + warp * (D * SB);
     const uint32_t *wp[R];
     const uint16_t *sp[R], *bp[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        // tiles past the last repeat it; their sums are not stored
-        const int m = a.pair ? r & 1 : 0, i = a.pair ? r >> 1 : r;
-        const long tile = min((long)blockIdx.x * per + i, (long)a.tiles - 1);
-        wp[r] = a.words[m] + tile * a.nsb * 256 + lane * 4;
-        sp[r] = a.scales[m] + (tile * a.nsb * 8 + g) * (2 * NG);
-        bp[r] = BIAS ? a.biases[m] + (tile * a.nsb * 8 + g) * (2 * NG) : nullptr;
+        const bool up = a.pair && (r & 1);
+        const long at = min((long)grp * per + (a.pair ? r >> 1 : r), (long)a.tiles - 1) * a.nsb + kw;
+        wp[r] = (up ? a.words[1] : a.words[0]) + at * 256 + lane * 4;
+        sp[r] = (up ? a.scales[1] : a.scales[0]) + (at * 8 + g) * (2 * NG);
+        bp[r] = BIAS ? (up ? a.biases[1] : a.biases[0]) + (at * 8 + g) * (2 * NG) : nullptr;
     }
-    const uint16_t *xp[NT];
-    bool live[NT];
+    auto fetch = [&](int sb, int stage) {
+        if (sb < a.nsb) {
+            const uint32_t at = base + stage * SB;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        live[n] = t0 + 8 * n + g < a.T;
-        xp[n] = a.x + (live[n] ? (long)(t0 + 8 * n + g) * a.x_ld : 0) + 8 * c;
-    }
+            for (int r = 0; r < R; ++r) {
+                copy_async<16>(at + r * 1024 + lane * 16, wp[r]);
+                copy_async<16>(at + r * 1024 + 512 + lane * 16, wp[r] + 128);
+                wp[r] += ks * 256;
+                if (c == 0) {
+                    copy_async<4 * NG>(at + R * 1024 + (r * 8 + g) * (4 * NG), sp[r]);
+                    if constexpr (BIAS)
+                        copy_async<4 * NG>(at + R * 1024 + ((R + r) * 8 + g) * (4 * NG), bp[r]);
+                }
+                sp[r] += ks * (16 * NG);
+                if constexpr (BIAS)
+                    bp[r] += ks * (16 * NG);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // x fragments of a column tile (of a span for 32 tokens). Tokens past the last read token 0 again (their results
+    // are not stored), spans past the last column its last span (their scales are 0).
+    const uint16_t *xp[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        xp[n] = a.x + (t0 + 8 * n + g < a.T ? (long)(t0 + 8 * n + g) * a.x_ld : 0) + 8 * c;
+    uint4 xv[NT < 4 ? 4 : 1][NT];
+    auto load_x = [&](int sb, int p, uint4 (&v)[NT]) {
+        const int k = min(sb * 128 + p * 32, a.cols - 32);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            v[n] = ldg_u128(xp[n] + k);
+    };
     float acc[R][NT][4];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -108,118 +181,142 @@ __global__ void __launch_bounds__(256) vq_q4_gemv_kernel(const Q4Args a)
             for (int j = 0; j < 4; ++j)
                 acc[r][n][j] = 0.f;
 
-    for (int sb = warp; sb < a.nsb; sb += warps) {
-        uint4 w[R][2];
+    grid_dep_launch();
+    grid_dep_wait();
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i)
+        fetch(kw + i * ks, i);
+    int stage = 0;
+    for (int sb = kw; sb < a.nsb; sb += ks) {
+        if constexpr (NT < 4) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                load_x(sb, p, xv[p]);
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory");
+        __syncwarp();   // the stage's scales came through other lanes, and all lanes are done with the stage refilled next
+        fetch(sb + (D - 1) * ks, stage == 0 ? D - 1 : stage - 1);
+        const uint32_t at = base + stage * SB;
+        stage = stage == D - 1 ? 0 : stage + 1;
         uint32_t sc[R][NG], bi[R][NG];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            w[r][0] = ldg_u128(wp[r] + (long)sb * 256);
-            w[r][1] = ldg_u128(wp[r] + (long)sb * 256 + 128);
-            load_pairs<NG>(sp[r] + (long)sb * (16 * NG), sc[r]);
+            lds_pairs<NG>(at + R * 1024 + (r * 8 + g) * (4 * NG), sc[r]);
             if constexpr (BIAS)
-                load_pairs<NG>(bp[r] + (long)sb * (16 * NG), bi[r]);
+                lds_pairs<NG>(at + R * 1024 + ((R + r) * 8 + g) * (4 * NG), bi[r]);
         }
         float part[R][NT][4], xs[NT][4];
+        uint4 w[R];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {   // 32-column spans
-            if (p % SPANS == 0) {
+            if ((p & 1) == 0) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            part[r][n][j] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        xs[n][j] = 0.f;
-                }
+                for (int r = 0; r < R; ++r)
+                    w[r] = lds128(at + r * 1024 + (p >> 1) * 512 + lane * 16);
             }
-            const int k0 = sb * 128 + p * 32;
-            uint4 xv[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                xv[n] = live[n] && k0 < a.cols ? ldg_u128(xp[n] + k0) : make_uint4(0, 0, 0, 0);
+            if constexpr (NT == 4)
+                load_x(sb, p, xv[0]);
+            constexpr int XP = NT < 4 ? 1 : 0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                const bool first = p % SPANS == 0 && h == 0;   // a group's sums start from zero
+                const uint32_t ones[4] = {BF16_ONES, BF16_ONES, BF16_ONES, BF16_ONES};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint4 &x = xv[XP * p][n];
+                    mma_bf16(xs[n], ones, h ? x.z : x.x, h ? x.w : x.y, first);
+                }
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const uint4 q = w[r][p >> 1];
-                    const uint32_t word = (p & 1) ? (h ? q.w : q.z) : (h ? q.y : q.x);
+                    const uint32_t word = (p & 1) ? (h ? w[r].w : w[r].z) : (h ? w[r].y : w[r].x);
                     uint32_t A[4];
                     decode(word, A);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma_bf16(part[r][n], A, h ? xv[n].z : xv[n].x, h ? xv[n].w : xv[n].y);
-                }
-                if constexpr (BIAS) {
-                    const uint32_t A[4] = {BF16_ONES, BF16_ONES, BF16_ONES, BF16_ONES};
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma_bf16(xs[n], A, h ? xv[n].z : xv[n].x, h ? xv[n].w : xv[n].y);
+                    for (int n = 0; n < NT; ++n) {
+                        const uint4 &x = xv[XP * p][n];
+                        mma_bf16(part[r][n], A, h ? x.z : x.x, h ? x.w : x.y, first);
+                    }
                 }
             }
             if (p % SPANS == SPANS - 1) {
-                const int grp = p / SPANS;
+                const int gi = p / SPANS;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float2 s = half_pair(sc[r][grp]);
+                    const float2 s = half_pair(sc[r][gi]);
                     float2 b = make_float2(0.f, 0.f);
                     if constexpr (BIAS) {
-                        b = half_pair(bi[r][grp]);
+                        b = half_pair(bi[r][gi]);
                         b = make_float2(fmaf(8.f, s.x, b.x), fmaf(8.f, s.y, b.y));
                     }
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        acc[r][n][0] = fmaf(s.x, part[r][n][0], acc[r][n][0]);
-                        acc[r][n][1] = fmaf(s.x, part[r][n][1], acc[r][n][1]);
-                        acc[r][n][2] = fmaf(s.y, part[r][n][2], acc[r][n][2]);
-                        acc[r][n][3] = fmaf(s.y, part[r][n][3], acc[r][n][3]);
-                        if constexpr (BIAS) {
-                            acc[r][n][0] = fmaf(b.x, xs[n][0], acc[r][n][0]);
-                            acc[r][n][1] = fmaf(b.x, xs[n][1], acc[r][n][1]);
-                            acc[r][n][2] = fmaf(b.y, xs[n][2], acc[r][n][2]);
-                            acc[r][n][3] = fmaf(b.y, xs[n][3], acc[r][n][3]);
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float q = fmaf(-24.f, xs[n][j & 1], part[r][n][j]);   // sum (q - 8) x
+                            acc[r][n][j] = fmaf(j < 2 ? s.x : s.y, q, acc[r][n][j]);
+                            if constexpr (BIAS)
+                                acc[r][n][j] = fmaf(j < 2 ? b.x : b.y, xs[n][j & 1], acc[r][n][j]);
                         }
-                    }
                 }
             }
         }
     }
 
-    constexpr int V = R * NT * 4;
+    if (ks > 1) {
+        float *sums = reinterpret_cast<float *>(ring);
+        // every copy has landed (the last turns' groups are empty) and every warp is done with its ring
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sums[(warp * V + (r * NT + n) * 4 + j) * 32 + lane] = acc[r][n][j];
+        __syncthreads();
+        // the values are spread over the row group's warps, each adds its own in warp order; of a pair, the warp that
+        // stores a value needs both modules' sums
+        const float *s = sums + (size_t)(warp - kw) * V * 32;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int v = ((a.pair ? r >> 1 : r) * NT + n) * 4 + j;
+                    if ((v & (ks - 1)) == kw) {
+                        float t = 0.f;
+                        for (int w = 0; w < ks; ++w)
+                            t += s[(w * V + (r * NT + n) * 4 + j) * 32 + lane];
+                        acc[r][n][j] = t;
+                    }
+                }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (a.pair && (r & 1))
+            continue;
+        const int i = a.pair ? r >> 1 : r;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                sums[(warp * V + (r * NT + n) * 4 + j) * 32 + lane] = acc[r][n][j];
-    __syncthreads();
-    // outputs, rows fastest: (token, row of the CTA's tiles)
-    for (int o = threadIdx.x; o < per * 16 * 8 * NT; o += blockDim.x) {
-        const int rr = o % (per * 16), t = o / (per * 16);
-        const int i = rr >> 4, row16 = rr & 15, n = t >> 3, t8 = t & 7;
-        const int at = ((n * 4) + (row16 >> 3) * 2 + (t8 & 1)) * 32 + (row16 & 7) * 4 + (t8 >> 1);
-        const long row = ((long)blockIdx.x * per + i) * 16 + row16;
-        const int token = t0 + t;
-        if (row >= a.rows || token >= a.T)
-            continue;
-        float v[2] = {0.f, 0.f};
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            if (m && !a.pair)
-                break;
-            const int r = a.pair ? 2 * i + m : i;
-            for (int w = 0; w < warps; ++w)
-                v[m] += sums[(w * V + r * NT * 4) * 32 + at];
-        }
-        const float out = a.pair ? v[0] * sigmoid(v[0]) * v[1] : v[0];
-        const long yi = (long)token * a.y_ld + row;
-        if (a.y_dtype == VQ_F32)
-            static_cast<float *>(a.y)[yi] = out;
-        else
-            static_cast<uint16_t *>(a.y)[yi] = f32_to_bf16_bits(out);
+            for (int j = 0; j < 4; ++j) {
+                const int v = (i * NT + n) * 4 + j;
+                const long row = ((long)grp * per + i) * 16 + g + 8 * (j >> 1);
+                const int token = t0 + 8 * n + 2 * c + (j & 1);
+                if ((v & (ks - 1)) != kw || row >= a.rows || token >= a.T)
+                    continue;
+                float out = acc[r][n][j];
+                if constexpr (R > 1)
+                    if (a.pair)
+                        out = out * sigmoid(out) * acc[r | 1][n][j];
+                const long yi = (long)token * a.y_ld + row;
+                if (a.y_dtype == VQ_F32)
+                    static_cast<float *>(a.y)[yi] = out;
+                else
+                    static_cast<uint16_t *>(a.y)[yi] = f32_to_bf16_bits(out);
+            }
     }
 }
 
@@ -246,8 +343,8 @@ __global__ void __launch_bounds__(256) vq_q4_pack_kernel(const uint32_t *codes, 
 #pragma unroll
                 for (int pr = 0; pr < 2; ++pr) {   // columns k + 2 pr and k + 2 pr + 1
                     const int m = hi + 2 * pr;
-                    out |= ((w >> (8 * pr)) & 15u) << (4 * m);
-                    out |= ((w >> (8 * pr + 4)) & 15u) << (16 + 4 * m);
+                    const uint32_t both = ((w >> (8 * pr)) & 15u) | ((w >> (8 * pr + 4)) & 15u) << 16;
+                    out |= __funnelshift_l(both, both, 3 + 4 * m);
                 }
             }
         }
@@ -270,18 +367,29 @@ template <int R, int NT, int G, bool BIAS>
 cudaError_t run(const Q4Args &a, cudaStream_t s)
 {
     const int per = a.pair ? R / 2 : R;
-    const int warps = std::min(8, a.nsb);
-    const size_t smem = (size_t)warps * R * NT * 4 * 32 * 4;   // at most 32 KB
-    const dim3 grid((a.tiles + per - 1) / per, (a.T + 8 * NT - 1) / (8 * NT));
-    return launch_after(vq_q4_gemv_kernel<R, NT, G, BIAS>, grid, dim3(32 * warps), smem, s, a);
+    const long groups = (a.tiles + per - 1) / per;
+    // warps per row group: enough warps for the GPU, but no more than there are column tiles
+    int ks = 1;
+    while (ks < MAX_WARPS<R, NT> && 2 * ks <= a.nsb && groups * ks < Q4_WANT_WARPS)
+        ks *= 2;
+    const int warps = std::max(4, ks);
+    constexpr int PER_WARP = std::max(STAGES<R> * STAGE_BYTES<R, G, BIAS>, R * NT * 4 * 32 * 4);
+    static_assert(MAX_WARPS<R, NT> * PER_WARP <= 227 * 1024);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem((const void *)vq_q4_gemv_kernel<R, NT, G, BIAS>, MAX_WARPS<R, NT> * PER_WARP, allowed);
+    if (e != cudaSuccess)
+        return e;
+    const dim3 grid((unsigned)((groups + warps / ks - 1) / (warps / ks)), (a.T + 8 * NT - 1) / (8 * NT));
+    return launch_after(vq_q4_gemv_kernel<R, NT, G, BIAS>, grid, dim3(32 * warps), warps * PER_WARP, s, a, ks);
 }
 
 template <int G, bool BIAS>
 cudaError_t pick(const Q4Args &a, cudaStream_t s)
 {
     const int nt = a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
-    const int tiles = a.tiles * (a.pair ? 2 : 1);
-    const int r = nt < 4 && tiles >= 4 * 4 * 148 ? 4 : a.pair || tiles >= 2 * 2 * 148 ? 2 : 1;
+    const long tiles = (long)a.tiles * (a.pair ? 2 : 1);
+    // more row tiles per warp once R tiles a group still give every SM its warps (8 per group)
+    const int r = nt < 4 && tiles * 8 >= 4 * Q4_WANT_WARPS ? 4 : a.pair || tiles * 8 >= 2 * Q4_WANT_WARPS ? 2 : 1;
     switch (r * 8 + nt) {
     case 9: return run<1, 1, G, BIAS>(a, s);
     case 10: return run<1, 2, G, BIAS>(a, s);
