@@ -48,6 +48,15 @@ inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_
     return e;
 }
 
+// Launches kernel K with `smem` <= MOST bytes of dynamic shared memory.
+template <auto K, int MOST, typename... Args>
+cudaError_t launch_smem(dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args)
+{
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem((const void *)K, MOST, done);
+    return e != cudaSuccess ? e : launch_after(K, grid, block, smem, s, args...);
+}
+
 // ---------------------------------------------------------------- chunks of a row
 //
 // VEC consecutive elements of a row: 8 with 16-byte accesses, or 1.
@@ -145,6 +154,98 @@ struct AnyChunk {
             h.get(v);
     }
 };
+
+// A chunk of a norm's weight as fp32, offset added.
+__device__ __forceinline__ void load_weight(const void *p, int dtype, float offset, int c, float (&w)[8])
+{
+    AnyChunk<8> k;
+    k.load(p, dtype, c);
+    k.get(w, dtype);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        w[j] += offset;
+}
+
+// ---------------------------------------------------------------- asynchronous copies
+//
+// A thread's own ring of 16-byte pieces in shared memory: piece k of a stage
+// is `step` bytes (16 x threads) after piece k - 1, so a warp's accesses are
+// contiguous. Each thread copies and reads only its own pieces, so a copy
+// needs no barrier, only the thread's own wait.
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Waits until at most `pending` (0 to 2) of this thread's groups are in flight.
+__device__ __forceinline__ void copy_wait(int pending)
+{
+    if (pending == 2)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (pending == 1)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+// Pieces of a chunk of 8 elements.
+template <typename T>
+constexpr int PIECES = sizeof(T) / 2;
+
+template <typename T>
+__device__ __forceinline__ void ring_copy(uint32_t at, uint32_t step, const T *p)
+{
+    copy16(at, p);
+    if constexpr (PIECES<T> == 2)
+        copy16(at + step, p + 4);
+}
+
+template <typename T>
+__device__ __forceinline__ void ring_get(uint32_t at, uint32_t step, float (&v)[8])
+{
+    Chunk<T, 8> c;
+    if constexpr (PIECES<T> == 2) {
+        const uint4 a = lds128(at), b = lds128(at + step);
+        c.a = make_float4(__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w));
+        c.b = make_float4(__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w));
+    } else {
+        c.r = lds128(at);
+    }
+    c.get(v);
+}
+
+__device__ __forceinline__ void ring_put(uint32_t at, uint32_t step, const float (&v)[8])
+{
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + step), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
+}
+
+// The same for an array whose type is known at run time.
+__device__ __forceinline__ void ring_copy_any(uint32_t at, uint32_t step, const void *p, int dtype, long i)
+{
+    if (dtype == VQ_F32)
+        ring_copy(at, step, static_cast<const float *>(p) + i);
+    else
+        ring_copy(at, step, static_cast<const uint16_t *>(p) + i);
+}
+
+__device__ __forceinline__ void ring_get_any(uint32_t at, uint32_t step, int dtype, float (&v)[8])
+{
+    if (dtype == VQ_F32)
+        ring_get<float>(at, step, v);
+    else
+        ring_get<uint16_t>(at, step, v);
+}
 
 // ---------------------------------------------------------------- sums
 

@@ -9,19 +9,24 @@
 // and the output, so each array crosses HBM once; the time is that of the
 // bytes for many rows and of one load, one or two row sums and one store for
 // few.
+#include <algorithm>
+
 #include "vq_block.cuh"
 #include "vq_norm.h"
 
 namespace vq {
 namespace {
 
+// ---------------------------------------------------------------- any rows, element by element
+
 // Where a thread's i-th chunk of a row starts, for a row over W warps.
 template <int VEC>
 __device__ __forceinline__ int chunk_at(int i, int tid, int W) { return (tid + i * 32 * W) * VEC; }
 
-template <typename HT, int VEC, int NV>
-__global__ void __launch_bounds__(1024) vq_norm_pre_kernel(const NormPreArgs a)
+template <typename HT, int NV>
+__global__ void __launch_bounds__(1024) vq_norm_pre_scalar_kernel(const NormPreArgs a)
 {
+    constexpr int VEC = 1;
     __shared__ RowSum<1> rs;
     grid_dep_launch();
     grid_dep_wait();
@@ -76,9 +81,10 @@ __global__ void __launch_bounds__(1024) vq_norm_pre_kernel(const NormPreArgs a)
     }
 }
 
-template <typename YT, typename HT, int VEC, int NV>
-__global__ void __launch_bounds__(1024) vq_norm_post_kernel(const NormPostArgs a)
+template <typename YT, typename HT, int NV>
+__global__ void __launch_bounds__(1024) vq_norm_post_scalar_kernel(const NormPostArgs a)
 {
+    constexpr int VEC = 1;
     __shared__ RowSum<1> rs;
     grid_dep_launch();
     grid_dep_wait();
@@ -193,59 +199,316 @@ __global__ void __launch_bounds__(1024) vq_norm_post_kernel(const NormPostArgs a
     }
 }
 
-// Warps per row, and rows per CTA: rows of one warp share a CTA of 4 warps.
-struct RowShape {
+// ---------------------------------------------------------------- rows on 16-byte boundaries
+//
+// Persistent CTAs, two or more on an SM; each copies its next rows into shared
+// memory while it works on one. A thread's columns are the same in every row,
+// so the weights stay in its registers.
+
+template <typename HT, int NV>
+__global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_kernel(const NormPreArgs a, int S)
+{
+    __shared__ RowSum<1> rs;
+    extern __shared__ __align__(16) unsigned char ring[];
+    constexpr int PH = PIECES<HT>, P = NV * PH;
+    const int W = a.W, tid = threadIdx.x % (32 * W), R = blockDim.x / (32 * W), stride = gridDim.x * R;
+    const long row0 = (long)blockIdx.x * R + threadIdx.x / (32 * W);
+    const uint32_t step = blockDim.x * 16, base = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+    const int hop = 256 * W;   // elements from a thread's chunk to its next
+    const HT *h = static_cast<const HT *>(a.h) + row0 * a.h_ld + tid * 8;
+    uint16_t *x = a.x + row0 * a.x_ld + tid * 8;
+    bool in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        in[i] = chunk_at<8>(i, tid, W) < a.H;
+    long ahead = row0;   // the row the next copy is for
+    auto fetch = [&](int s) {
+        if (ahead < a.T) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in[i])
+                    ring_copy(base + (s * P + i * PH) * step, step, h + i * hop);
+            h += stride * a.h_ld;
+            ahead += stride;
+        }
+        copy_commit();
+    };
+    grid_dep_launch();
+    grid_dep_wait();
+    for (int s = 0; s < S - 1; ++s)
+        fetch(s);
+    float w[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (in[i])
+            load_weight(a.n.weight, a.n.dtype, a.n.offset, chunk_at<8>(i, tid, W), w[i]);
+    int turn = 0, s = 0;
+    for (long row = row0; row < a.T; row += stride) {
+        if (S == 1) {
+            fetch(0);
+            copy_wait(0);
+        } else {
+            copy_wait(S - 2);
+            fetch(s == 0 ? S - 1 : s - 1);
+        }
+        const uint32_t at = base + s * P * step;
+        s = s == S - 1 ? 0 : s + 1;
+        float v[NV][8], ss[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+                ring_get<HT>(at + i * PH * step, step, v[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
+            }
+        row_sum(ss, rs, W, turn);
+        const float r = rsqrtf(ss[0] * a.inv_h + a.n.eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[i][j] = v[i][j] * r * w[i][j];
+                Chunk<uint16_t, 8> o;
+                o.set(v[i]);
+                o.store(x + i * hop);
+            }
+        x += stride * a.x_ld;
+    }
+}
+
+template <typename YT, typename HT, int NV>
+__global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_kernel(const NormPostArgs a, int S)
+{
+    __shared__ RowSum<1> rs;
+    extern __shared__ __align__(16) unsigned char ring[];
+    // pieces of a stage: y, h, per-channel gates
+    constexpr int PY = PIECES<YT>, PH = PIECES<HT>, OH = NV * PY, OZ = OH + NV * PH;
+    const bool post = a.post.weight != nullptr, next = a.next.weight != nullptr;
+    const int pz = a.gate_mode != GATE_CHANNEL ? 0 : a.gate_dtype == VQ_F32 ? 2 : 1, P = OZ + NV * pz;
+    const int W = a.W, tid = threadIdx.x % (32 * W), R = blockDim.x / (32 * W), stride = gridDim.x * R;
+    const long row0 = (long)blockIdx.x * R + threadIdx.x / (32 * W);
+    const uint32_t step = blockDim.x * 16, base = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+    const int hop = 256 * W;   // elements from a thread's chunk to its next
+    const YT *y = static_cast<const YT *>(a.y) + row0 * a.y_ld + tid * 8;
+    const HT *h = static_cast<const HT *>(a.h) + row0 * a.h_ld + tid * 8;
+    HT *ho = static_cast<HT *>(a.h_out) + row0 * a.ho_ld + tid * 8;
+    uint16_t *x = a.x + row0 * a.x_ld + tid * 8;
+    bool in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        in[i] = chunk_at<8>(i, tid, W) < a.H;
+    long ahead = row0;   // the row the next copy is for
+    auto fetch = [&](int s) {
+        if (ahead < a.T) {
+            const uint32_t at = base + s * P * step;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in[i]) {
+                    ring_copy(at + i * PY * step, step, y + i * hop);
+                    ring_copy(at + (OH + i * PH) * step, step, h + i * hop);
+                    if (pz)
+                        ring_copy_any(at + (OZ + i * pz) * step, step, a.gate, a.gate_dtype,
+                                      ahead * a.gate_ld + tid * 8 + i * hop);
+                }
+            y += stride * a.y_ld;
+            h += stride * a.h_ld;
+            ahead += stride;
+        }
+        copy_commit();
+    };
+    grid_dep_launch();
+    grid_dep_wait();
+    for (int s = 0; s < S - 1; ++s)
+        fetch(s);
+    float w1[NV][8], w2[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            w1[i][j] = w2[i][j] = 1.f;
+        if (in[i]) {
+            if (post)
+                load_weight(a.post.weight, a.post.dtype, a.post.offset, chunk_at<8>(i, tid, W), w1[i]);
+            if (next)
+                load_weight(a.next.weight, a.next.dtype, a.next.offset, chunk_at<8>(i, tid, W), w2[i]);
+        }
+    }
+    int turn = 0, s = 0;
+    for (long row = row0; row < a.T; row += stride) {
+        float f = a.out_scale;   // the branch's factor, but for the weight and a channel's gate
+        if (a.gate_mode == GATE_TOKEN) {
+            AnyChunk<1> z;
+            float v[1];
+            z.load(a.gate, a.gate_dtype, row * a.gate_ld);
+            z.get(v, a.gate_dtype);
+            f *= sigmoid(v[0]);
+        }
+        if (S == 1) {
+            fetch(0);
+            copy_wait(0);
+        } else {
+            copy_wait(S - 2);
+            fetch(s == 0 ? S - 1 : s - 1);
+        }
+        const uint32_t at = base + s * P * step;
+        s = s == S - 1 ? 0 : s + 1;
+        float u[NV][8], ss[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+                ring_get<YT>(at + i * PY * step, step, u[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    ss[0] = fmaf(u[i][j], u[i][j], ss[0]);
+            }
+        if (post) {
+            row_sum(ss, rs, W, turn);
+            f *= rsqrtf(ss[0] * a.inv_h + a.post.eps);
+        }
+        ss[0] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+                float v[8];
+                ring_get<HT>(at + (OH + i * PH) * step, step, v);
+                if (pz) {
+                    float z[8];
+                    ring_get_any(at + (OZ + i * pz) * step, step, a.gate_dtype, z);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        u[i][j] *= sigmoid(z[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = fmaf(u[i][j] * f, w1[i][j], a.res_scale * v[j]);
+                Chunk<HT, 8> o;
+                o.set(v);   // the row as stored: what the next norm sees
+                o.store(ho + i * hop);
+                o.get(u[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    ss[0] = fmaf(u[i][j], u[i][j], ss[0]);
+            }
+        ho += stride * a.ho_ld;
+        if (next) {
+            row_sum(ss, rs, W, turn);
+            const float r2 = rsqrtf(ss[0] * a.inv_h + a.next.eps);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in[i]) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        u[i][j] = u[i][j] * r2 * w2[i][j];
+                    Chunk<uint16_t, 8> o;
+                    o.set(u[i]);
+                    o.store(x + i * hop);
+                }
+            x += stride * a.x_ld;
+        }
+    }
+}
+
+// Scalar rows: as many threads as elements, up to 16 elements each.
+struct ScalarShape {
     int W, R, nv;
 };
 
-RowShape row_shape(int H, int vec, int T)
+ScalarShape scalar_shape(int H)
 {
-    RowShape s;
-    const int chunks = (H + vec - 1) / vec;
-    const int wide = vec == 8 ? 2 : 16;                       // most chunks per thread
-    int nv = 1;
-    while (nv < wide && (chunks + nv - 1) / nv > 1024)
-        nv = nv == 1 && vec == 1 ? 4 : nv * (vec == 8 ? 2 : 4);
-    s.nv = nv;
-    s.W = ((chunks + nv - 1) / nv + 31) / 32;
+    ScalarShape s;
+    s.nv = H <= 1024 ? 1 : H <= 4096 ? 4 : 16;
+    s.W = ((H + s.nv - 1) / s.nv + 31) / 32;
     s.R = s.W == 1 ? 4 : 1;
-    (void)T;
     return s;
+}
+
+constexpr int PRE_REGS[4] = {48, 64, 80, 104}, POST_REGS[4] = {64, 88, 112, 128};
+
+template <auto K, typename Args>
+cudaError_t rows(const NormShape &sh, cudaStream_t s, const Args &a)
+{
+    return launch_smem<K, NORM_SMEM>(dim3(sh.ctas), dim3(32 * sh.W * sh.R), sh.smem, s, a, sh.S);
 }
 
 template <typename HT>
 cudaError_t pre_launch(NormPreArgs a, bool vec8, cudaStream_t s)
 {
-    const RowShape sh = row_shape(a.H, vec8 ? 8 : 1, a.T);
-    a.W = sh.W;
-    const dim3 grid((unsigned)(((long)a.T + sh.R - 1) / sh.R)), block(32 * sh.W * sh.R);
-    if (vec8)
-        return sh.nv == 1 ? launch_after(vq_norm_pre_kernel<HT, 8, 1>, grid, block, 0, s, a)
-                          : launch_after(vq_norm_pre_kernel<HT, 8, 2>, grid, block, 0, s, a);
-    switch (sh.nv) {
-    case 1: return launch_after(vq_norm_pre_kernel<HT, 1, 1>, grid, block, 0, s, a);
-    case 4: return launch_after(vq_norm_pre_kernel<HT, 1, 4>, grid, block, 0, s, a);
-    default: return launch_after(vq_norm_pre_kernel<HT, 1, 16>, grid, block, 0, s, a);
+    const NormShape sh = norm_shape(a.H, a.T, sizeof(HT), 0, PRE_REGS, 256, 0);
+    if (vec8 && sh.S > 0) {
+        a.W = sh.W;
+        switch (sh.nv) {
+        case 1: return rows<vq_norm_pre_kernel<HT, 1>>(sh, s, a);
+        case 2: return rows<vq_norm_pre_kernel<HT, 2>>(sh, s, a);
+        case 3: return rows<vq_norm_pre_kernel<HT, 3>>(sh, s, a);
+        default: return rows<vq_norm_pre_kernel<HT, 4>>(sh, s, a);
+        }
     }
+    const ScalarShape sc = scalar_shape(a.H);
+    a.W = sc.W;
+    const dim3 grid((unsigned)(((long)a.T + sc.R - 1) / sc.R)), block(32 * sc.W * sc.R);
+    return sc.nv == 1   ? launch_after(vq_norm_pre_scalar_kernel<HT, 1>, grid, block, 0, s, a)
+           : sc.nv == 4 ? launch_after(vq_norm_pre_scalar_kernel<HT, 4>, grid, block, 0, s, a)
+                        : launch_after(vq_norm_pre_scalar_kernel<HT, 16>, grid, block, 0, s, a);
 }
 
 template <typename YT, typename HT>
 cudaError_t post_launch(NormPostArgs a, bool vec8, cudaStream_t s)
 {
-    const RowShape sh = row_shape(a.H, vec8 ? 8 : 1, a.T);
-    a.W = sh.W;
-    const dim3 grid((unsigned)(((long)a.T + sh.R - 1) / sh.R)), block(32 * sh.W * sh.R);
-    if (vec8)
-        return sh.nv == 1 ? launch_after(vq_norm_post_kernel<YT, HT, 8, 1>, grid, block, 0, s, a)
-                          : launch_after(vq_norm_post_kernel<YT, HT, 8, 2>, grid, block, 0, s, a);
-    switch (sh.nv) {
-    case 1: return launch_after(vq_norm_post_kernel<YT, HT, 1, 1>, grid, block, 0, s, a);
-    case 4: return launch_after(vq_norm_post_kernel<YT, HT, 1, 4>, grid, block, 0, s, a);
-    default: return launch_after(vq_norm_post_kernel<YT, HT, 1, 16>, grid, block, 0, s, a);
+    const int gate = a.gate_mode != GATE_CHANNEL ? 0 : a.gate_dtype == VQ_F32 ? 4 : 2;
+    const NormShape sh = norm_shape(a.H, a.T, sizeof(YT) + sizeof(HT) + gate, 0, POST_REGS, 256, 0);
+    if (vec8 && sh.S > 0) {
+        a.W = sh.W;
+        switch (sh.nv) {
+        case 1: return rows<vq_norm_post_kernel<YT, HT, 1>>(sh, s, a);
+        case 2: return rows<vq_norm_post_kernel<YT, HT, 2>>(sh, s, a);
+        case 3: return rows<vq_norm_post_kernel<YT, HT, 3>>(sh, s, a);
+        default: return rows<vq_norm_post_kernel<YT, HT, 4>>(sh, s, a);
+        }
     }
+    const ScalarShape sc = scalar_shape(a.H);
+    a.W = sc.W;
+    const dim3 grid((unsigned)(((long)a.T + sc.R - 1) / sc.R)), block(32 * sc.W * sc.R);
+    return sc.nv == 1   ? launch_after(vq_norm_post_scalar_kernel<YT, HT, 1>, grid, block, 0, s, a)
+           : sc.nv == 4 ? launch_after(vq_norm_post_scalar_kernel<YT, HT, 4>, grid, block, 0, s, a)
+                        : launch_after(vq_norm_post_scalar_kernel<YT, HT, 16>, grid, block, 0, s, a);
 }
 
 }  // namespace
+
+NormShape norm_shape(int H, int T, int bytes, int fixed, const int (&regs)[4], int threads, int max_ctas)
+{
+    NormShape s;
+    const int chunks = (H + 7) / 8;
+    // rows that stream take fewer threads with more elements each (the row sums and the addresses cost by the warp);
+    // with at most a row or two per SM a row takes as many threads as it can use
+    if (T <= 2 * 148 || chunks > 4 * threads)
+        threads = ROW_THREADS;
+    s.nv = (chunks + threads - 1) / threads;
+    s.W = ((chunks + s.nv - 1) / s.nv + 31) / 32;
+    s.R = s.W == 1 ? 8 : 1;
+    const int block = 32 * s.W * s.R;
+    const size_t row = (size_t)block * 8 * s.nv, stage = row * bytes, keep = row * fixed, room = NORM_SMEM;
+    s.S = s.ctas = 0;
+    s.smem = 0;
+    if (stage + keep > room)
+        return s;
+    // two rows ahead where they fit, then as many CTAs as registers and shared memory allow
+    int per_sm = std::max(1, std::min(16, 65536 / (regs[s.nv - 1] * block)));
+    while (per_sm > 1 && per_sm * (2 * stage + keep) > room)
+        --per_sm;
+    s.S = (int)std::min<size_t>(4, (room / per_sm - keep) / stage);
+    long ctas = std::min(((long)T + s.R - 1) / s.R, 148L * per_sm);
+    if (max_ctas)
+        ctas = std::min<long>(ctas, max_ctas);
+    s.ctas = (int)std::max(1L, ctas);
+    // no more stages than a CTA has rows
+    const long rows = ((long)T + (long)s.ctas * s.R - 1) / ((long)s.ctas * s.R);
+    s.S = (int)std::min<long>(s.S, std::max(1L, rows));
+    s.smem = s.S * stage + keep;
+    return s;
+}
 
 cudaError_t launch_norm_pre(const NormPreArgs &a, int h_dtype, bool vec8, cudaStream_t s)
 {

@@ -21,6 +21,14 @@ enum { GATE_NONE = 0, GATE_TOKEN = 1, GATE_CHANNEL = 2 };
 
 #ifdef __CUDACC__
 __device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+
+// sigmoid(z) and sigmoid(-z) from one exponential and one division by a number in [1, 2].
+__device__ __forceinline__ void sigmoids(float z, float &on, float &off)
+{
+    const float e = expf(-fabsf(z)), s = __fdividef(1.f, 1.f + e), r = e * s;
+    on = z < 0.f ? r : s;
+    off = z < 0.f ? s : r;
+}
 #endif
 
 struct NormPreArgs {
@@ -65,6 +73,19 @@ struct NormPostBwdArgs {
     int T, H, W;
     float inv_h, res_scale, out_scale;
 };
+
+// How a launch of the ring kernels covers the rows: W warps a row, R rows side
+// by side in a CTA, nv chunks of 8 elements a thread, S rows of shared memory
+// (S - 1 copied ahead), `ctas` persistent CTAs. S = 0: a row does not fit.
+struct NormShape {
+    int W, R, nv, S, ctas;
+    size_t smem;
+};
+constexpr int ROW_THREADS = 512;           // most threads a row
+constexpr int NORM_SMEM = 208 * 1024;      // shared memory of an SM given to the rings
+// bytes: of input an element copied ahead; fixed: bytes an element kept for the whole launch; regs: registers a
+// thread at nv chunks (regs[nv - 1]); threads: a row's threads when rows stream; max_ctas: 0, or the most CTAs.
+NormShape norm_shape(int H, int T, int bytes, int fixed, const int (&regs)[4], int threads, int max_ctas);
 
 // vec8: every row (pointers and strides) on 16-byte boundaries and H a multiple of 8.
 cudaError_t launch_norm_pre(const NormPreArgs &a, int h_dtype, bool vec8, cudaStream_t s);

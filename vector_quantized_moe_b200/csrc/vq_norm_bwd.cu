@@ -15,15 +15,15 @@
 namespace vq {
 namespace {
 
-constexpr int BWD_THREADS = 512;    // most threads per CTA: 128 registers each
-constexpr int NORM_PARTS = 592;     // most partial rows (4 per SM of 148)
+constexpr int NORM_PARTS = 592;     // most partial rows: 4 CTAs on each of 148 SMs
 
 template <int VEC>
 __device__ __forceinline__ int chunk_at(int i, int tid, int W) { return (tid + i * 32 * W) * VEC; }
 
-template <typename HT, int VEC, int NV>
-__global__ void __launch_bounds__(BWD_THREADS) vq_norm_pre_bwd_kernel(const NormPreBwdArgs a)
+template <typename HT, int NV>
+__global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_bwd_scalar_kernel(const NormPreBwdArgs a)
 {
+    constexpr int VEC = 1;
     __shared__ RowSum<2> rs;
     grid_dep_launch();
     grid_dep_wait();
@@ -111,9 +111,10 @@ __global__ void __launch_bounds__(BWD_THREADS) vq_norm_pre_bwd_kernel(const Norm
     }
 }
 
-template <typename YT, typename HT, int VEC, int NV>
-__global__ void __launch_bounds__(BWD_THREADS) vq_norm_post_bwd_kernel(const NormPostBwdArgs a)
+template <typename YT, typename HT, int NV>
+__global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_scalar_kernel(const NormPostBwdArgs a)
 {
+    constexpr int VEC = 1;
     __shared__ RowSum<3> rs;
     grid_dep_launch();
     grid_dep_wait();
@@ -306,6 +307,374 @@ __global__ void __launch_bounds__(BWD_THREADS) vq_norm_post_bwd_kernel(const Nor
     }
 }
 
+// ---------------------------------------------------------------- rows on 16-byte boundaries, copied ahead
+
+// A CTA's weight gradient: its side-by-side rows' sums added in order into one partial row.
+template <int NV>
+__device__ __forceinline__ void write_part(float *part, const float (&acc)[NV][8], float *side, int tid, int W, int H)
+{
+    const int R = blockDim.x / (32 * W), rg = threadIdx.x / (32 * W);
+    if (R > 1) {   // one-warp rows (NV = 1): side is [R][256]
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            side[rg * 256 + tid * 8 + j] = acc[0][j];
+        __syncthreads();
+        for (int c = threadIdx.x; c < H; c += blockDim.x) {
+            float v = side[c];
+            for (int r = 1; r < R; ++r)
+                v += side[r * 256 + c];
+            part[(long)blockIdx.x * H + c] = v;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = chunk_at<8>(i, tid, W);
+        if (c < H) {
+            Chunk<float, 8> o;
+            o.set(acc[i]);
+            o.store(part + (long)blockIdx.x * H + c);
+        }
+    }
+}
+
+template <typename HT, int NV>
+__global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_bwd_kernel(const NormPreBwdArgs a, int S)
+{
+    __shared__ RowSum<2> rs;
+    __shared__ float side[NV == 1 ? 8 * 256 : 1];
+    extern __shared__ __align__(16) unsigned char ring[];
+    constexpr int PH = PIECES<HT>, OX = NV * PH, OR = OX + NV;   // pieces: h, dx, dres
+    const bool res = a.dres != nullptr;
+    const int P = OR + (res ? NV * PH : 0);
+    const int W = a.W, tid = threadIdx.x % (32 * W), R = blockDim.x / (32 * W), stride = gridDim.x * R;
+    const long row0 = (long)blockIdx.x * R + threadIdx.x / (32 * W);
+    const uint32_t step = blockDim.x * 16, base = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+    const int hop = 256 * W;   // elements from a thread's chunk to its next
+    const HT *h = static_cast<const HT *>(a.h) + row0 * a.h_ld + tid * 8;
+    const HT *dres = static_cast<const HT *>(a.dres) + row0 * a.dres_ld + tid * 8;
+    const uint16_t *dx = a.dx + row0 * a.dx_ld + tid * 8;
+    HT *dh = static_cast<HT *>(a.dh) + row0 * a.dh_ld + tid * 8;
+    bool in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        in[i] = chunk_at<8>(i, tid, W) < a.H;
+    long ahead = row0;   // the row the next copy is for
+    auto fetch = [&](int s) {
+        if (ahead < a.T) {
+            const uint32_t at = base + s * P * step;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in[i]) {
+                    ring_copy(at + i * PH * step, step, h + i * hop);
+                    ring_copy(at + (OX + i) * step, step, dx + i * hop);
+                    if (res)
+                        ring_copy(at + (OR + i * PH) * step, step, dres + i * hop);
+                }
+            h += stride * a.h_ld;
+            dx += stride * a.dx_ld;
+            dres += stride * a.dres_ld;
+            ahead += stride;
+        }
+        copy_commit();
+    };
+    grid_dep_launch();
+    grid_dep_wait();
+    for (int s = 0; s < S - 1; ++s)
+        fetch(s);
+    float acc[NV][8], w[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (in[i])
+            load_weight(a.n.weight, a.n.dtype, a.n.offset, chunk_at<8>(i, tid, W), w[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            acc[i][j] = 0.f;
+    }
+    int turn = 0, s = 0;
+    for (long row = row0; row < a.T; row += stride) {
+        if (S == 1) {
+            fetch(0);
+            copy_wait(0);
+        } else {
+            copy_wait(S - 2);
+            fetch(s == 0 ? S - 1 : s - 1);
+        }
+        const uint32_t at = base + s * P * step;
+        s = s == S - 1 ? 0 : s + 1;
+        float q[2] = {0.f, 0.f};   // |h|^2, sum g h
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+                float v[8], d[8];
+                ring_get<HT>(at + i * PH * step, step, v);
+                ring_get<uint16_t>(at + (OX + i) * step, step, d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    q[0] = fmaf(v[j], v[j], q[0]);
+                    q[1] = fmaf(d[j] * w[i][j], v[j], q[1]);
+                }
+            }
+        row_sum(q, rs, W, turn);
+        const float r = rsqrtf(q[0] * a.inv_h + a.n.eps);
+        const float rm = r * (r * (q[1] * a.inv_h));   // r mean(g v^)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+                float v[8], d[8], o[8];
+                ring_get<HT>(at + i * PH * step, step, v);
+                ring_get<uint16_t>(at + (OX + i) * step, step, d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    o[j] = 0.f;
+                if (res)
+                    ring_get<HT>(at + (OR + i * PH) * step, step, o);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float n = v[j] * r;
+                    acc[i][j] = fmaf(d[j], n, acc[i][j]);
+                    o[j] += fmaf(-n, rm, r * (d[j] * w[i][j]));   // r (g - v^ mean(g v^))
+                }
+                Chunk<HT, 8> oc;
+                oc.set(o);
+                oc.store(dh + i * hop);
+            }
+        dh += stride * a.dh_ld;
+    }
+    if (a.part)
+        write_part(a.part, acc, side, tid, W, a.H);
+}
+
+// The weights (offset added, fp32) of a thread's columns sit in shared memory
+// behind the ring: with two weight gradients a thread has no registers for them.
+template <typename YT, typename HT, int NV>
+__global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const NormPostBwdArgs a, int S)
+{
+    __shared__ RowSum<3> rs;
+    __shared__ float side[NV == 1 ? 8 * 256 : 1];
+    extern __shared__ __align__(16) unsigned char ring[];
+    const bool post = a.post.weight != nullptr, next = a.next.weight != nullptr, has = a.dho != nullptr;
+    // pieces of a stage: y, dh_out, h_out and dx_out (with the next norm), per-channel gates
+    constexpr int PY = PIECES<YT>, PH = PIECES<HT>, OG = NV * PY;
+    const int OH = OG + (has ? NV * PH : 0), OX = OH + (next ? NV * PH : 0), OZ = OX + (next ? NV : 0);
+    const int pz = a.gate_mode != GATE_CHANNEL ? 0 : a.gate_dtype == VQ_F32 ? 2 : 1, P = OZ + NV * pz;
+    const int W = a.W, tid = threadIdx.x % (32 * W), R = blockDim.x / (32 * W), stride = gridDim.x * R;
+    const long row0 = (long)blockIdx.x * R + threadIdx.x / (32 * W);
+    const uint32_t step = blockDim.x * 16, base = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+    const uint32_t at1 = base + S * P * step, at2 = at1 + (post ? 2 * NV * step : 0);   // the weights
+    const int hop = 256 * W;   // elements from a thread's chunk to its next
+    const YT *y = static_cast<const YT *>(a.y) + row0 * a.y_ld + tid * 8;
+    const HT *h = static_cast<const HT *>(a.h) + row0 * a.h_ld + tid * 8;
+    const HT *dho = static_cast<const HT *>(a.dho) + row0 * a.dho_ld + tid * 8;
+    const uint16_t *dx = a.dx + row0 * a.dx_ld + tid * 8;
+    YT *dy = static_cast<YT *>(a.dy) + row0 * a.dy_ld + tid * 8;
+    HT *dh = static_cast<HT *>(a.dh) + row0 * a.dh_ld + tid * 8;
+    bool in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        in[i] = chunk_at<8>(i, tid, W) < a.H;
+    long ahead = row0;   // the row the next copy is for
+    auto fetch = [&](int s) {
+        if (ahead < a.T) {
+            const uint32_t at = base + s * P * step;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in[i]) {
+                    ring_copy(at + i * PY * step, step, y + i * hop);
+                    if (has)
+                        ring_copy(at + (OG + i * PH) * step, step, dho + i * hop);
+                    if (next) {
+                        ring_copy(at + (OH + i * PH) * step, step, h + i * hop);
+                        ring_copy(at + (OX + i) * step, step, dx + i * hop);
+                    }
+                    if (pz)
+                        ring_copy_any(at + (OZ + i * pz) * step, step, a.gate, a.gate_dtype,
+                                      ahead * a.gate_ld + tid * 8 + i * hop);
+                }
+            y += stride * a.y_ld;
+            h += stride * a.h_ld;
+            dho += stride * a.dho_ld;
+            dx += stride * a.dx_ld;
+            ahead += stride;
+        }
+        copy_commit();
+    };
+    grid_dep_launch();
+    grid_dep_wait();
+    for (int s = 0; s < S - 1; ++s)
+        fetch(s);
+    float acc1[NV][8], acc2[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float w[8];
+        if (in[i] && post) {
+            load_weight(a.post.weight, a.post.dtype, a.post.offset, chunk_at<8>(i, tid, W), w);
+            ring_put(at1 + 2 * i * step, step, w);
+        }
+        if (in[i] && next) {
+            load_weight(a.next.weight, a.next.dtype, a.next.offset, chunk_at<8>(i, tid, W), w);
+            ring_put(at2 + 2 * i * step, step, w);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            acc1[i][j] = acc2[i][j] = 0.f;
+    }
+    int turn = 0, s = 0;
+    for (long row = row0; row < a.T; row += stride) {
+        float on = 1.f, off = 0.f;   // sigmoid(z), 1 - sigmoid(z)
+        if (a.gate_mode == GATE_TOKEN) {
+            AnyChunk<1> z;
+            float v[1];
+            z.load(a.gate, a.gate_dtype, row * a.gate_ld);
+            z.get(v, a.gate_dtype);
+            sigmoids(v[0], on, off);
+        }
+        if (S == 1) {
+            fetch(0);
+            copy_wait(0);
+        } else {
+            copy_wait(S - 2);
+            fetch(s == 0 ? S - 1 : s - 1);
+        }
+        const uint32_t at = base + s * P * step;
+        s = s == S - 1 ? 0 : s + 1;
+        // the sums that need nothing but the inputs: |h'|^2, sum g h' of the next norm, |y|^2
+        float q[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+                float v[8], d[8], w[8];
+                if (next) {
+                    ring_get<HT>(at + (OH + i * PH) * step, step, v);
+                    ring_get<uint16_t>(at + (OX + i) * step, step, d);
+                    ring_get<float>(at2 + 2 * i * step, step, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        q[0] = fmaf(v[j], v[j], q[0]);
+                        q[1] = fmaf(d[j] * w[j], v[j], q[1]);
+                    }
+                }
+                if (post) {
+                    ring_get<YT>(at + i * PY * step, step, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        q[2] = fmaf(v[j], v[j], q[2]);
+                }
+            }
+        if (next || post)
+            row_sum(q, rs, W, turn);
+        const float r2 = rsqrtf(q[0] * a.inv_h + a.next.eps), rm2 = r2 * (r2 * (q[1] * a.inv_h));
+        const float r1 = post ? rsqrtf(q[2] * a.inv_h + a.post.eps) : 1.f;
+        const float f = a.out_scale * on;   // du = f dH but for a channel's gate
+        float dH[NV][8], t[2] = {0.f, 0.f};   // sums: g y of the post norm, du u
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+                float v[8], w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    dH[i][j] = 0.f;
+                if (has)
+                    ring_get<HT>(at + (OG + i * PH) * step, step, dH[i]);
+                if (next) {
+                    float d[8];
+                    ring_get<HT>(at + (OH + i * PH) * step, step, v);
+                    ring_get<uint16_t>(at + (OX + i) * step, step, d);
+                    ring_get<float>(at2 + 2 * i * step, step, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float n = v[j] * r2;
+                        acc2[i][j] = fmaf(d[j], n, acc2[i][j]);
+                        dH[i][j] += fmaf(-n, rm2, r2 * (d[j] * w[j]));
+                    }
+                }
+                if (a.dh) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[j] = a.res_scale * dH[i][j];
+                    Chunk<HT, 8> oc;
+                    oc.set(v);
+                    oc.store(dh + i * hop);
+                }
+                ring_get<YT>(at + i * PY * step, step, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[j] = 1.f;
+                if (post)
+                    ring_get<float>(at1 + 2 * i * step, step, w);
+                if (pz) {
+                    float z[8];
+                    ring_get_any(at + (OZ + i * pz) * step, step, a.gate_dtype, z);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float zon, zoff;
+                        sigmoids(z[j], zon, zoff);
+                        const float du = f * dH[i][j] * zon, n = v[j] * r1;
+                        z[j] = du * zoff * (n * w[j]);   // dv u s (1 - s)
+                        acc1[i][j] = fmaf(du, n, acc1[i][j]);
+                        dH[i][j] = du * w[j];            // g
+                        t[0] = fmaf(dH[i][j], v[j], t[0]);
+                    }
+                    if (a.dgate) {
+                        const long to = row * a.dgate_ld + tid * 8 + i * hop;
+                        if (a.gate_dtype == VQ_F32) {
+                            Chunk<float, 8> oc;
+                            oc.set(z);
+                            oc.store(static_cast<float *>(a.dgate) + to);
+                        } else {
+                            Chunk<uint16_t, 8> oc;
+                            oc.set(z);
+                            oc.store(static_cast<uint16_t *>(a.dgate) + to);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float du = a.out_scale * dH[i][j], n = v[j] * r1;   // dv
+                        acc1[i][j] = fmaf(du * on, n, acc1[i][j]);
+                        const float dn = du * w[j];
+                        t[1] = fmaf(dn, n, t[1]);                                 // dv u
+                        dH[i][j] = dn * on;                                       // g
+                    }
+                }
+            }
+        dh += stride * a.dh_ld;
+        const bool token = a.gate_mode == GATE_TOKEN && a.dgate;
+        if (post || token)
+            row_sum(t, rs, W, turn);
+        if (token && tid == 0) {
+            const float dz = t[1] * on * off;
+            const long to = row * a.dgate_ld;
+            if (a.gate_dtype == VQ_F32)
+                static_cast<float *>(a.dgate)[to] = dz;
+            else
+                static_cast<uint16_t *>(a.dgate)[to] = f32_to_bf16_bits(dz);
+        }
+        // r1 mean(g y^): from sum g y, or from sum dv u = sum (g / on) y^
+        const float rm1 = r1 * ((pz ? r1 * t[0] : on * t[1]) * a.inv_h);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+                if (post) {
+                    float v[8];
+                    ring_get<YT>(at + i * PY * step, step, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        dH[i][j] = fmaf(-(v[j] * r1), rm1, r1 * dH[i][j]);
+                }
+                Chunk<YT, 8> oc;
+                oc.set(dH[i]);
+                oc.store(dy + i * hop);
+            }
+        dy += stride * a.dy_ld;
+    }
+    if (a.part1)
+        write_part(a.part1, acc1, side, tid, W, a.H);
+    if (a.part2)
+        write_part(a.part2, acc2, side, tid, W, a.H);
+}
+
 // Column sums of the partial rows, in row order within each of 8 interleaved
 // strands, then over the strands: d[c] = sum_p part[p][c]. blockIdx.y: which
 // weight gradient.
@@ -336,111 +705,121 @@ __global__ void __launch_bounds__(256) vq_norm_dw_kernel(const float *p1, float 
     }
 }
 
-struct BwdShape {
-    int W, R, nv, ctas, parts;
-};
-
-BwdShape bwd_shape(int H, int vec, int T)
+// Scalar rows: up to 32 elements a thread.
+NormShape scalar_shape(int H, int T)
 {
-    BwdShape s;
-    const int chunks = (H + vec - 1) / vec;
-    int nv = 1;
-    while ((chunks + nv - 1) / nv > BWD_THREADS)
-        nv = vec == 8 ? nv * 2 : nv == 1 ? 8 : 32;
-    s.nv = nv;
-    s.W = ((chunks + nv - 1) / nv + 31) / 32;
+    NormShape s{};
+    s.nv = H <= ROW_THREADS ? 1 : H <= 8 * ROW_THREADS ? 8 : 32;
+    s.W = ((H + s.nv - 1) / s.nv + 31) / 32;
     s.R = s.W == 1 ? 4 : 1;
-    s.ctas = std::max(1, (int)std::min(((long)T + s.R - 1) / s.R, (long)NORM_PARTS / s.R));
-    s.parts = s.ctas * s.R;
+    s.ctas = (int)std::max(1L, std::min(((long)T + s.R - 1) / s.R, (long)NORM_PARTS / s.R));
     return s;
 }
 
-cudaError_t finish(const BwdShape &sh, int T, int H, const float *p1, float *d1, const float *p2, float *d2,
-                   cudaStream_t s)
+cudaError_t finish(int parts, int H, const float *p1, float *d1, const float *p2, float *d2, cudaStream_t s)
 {
     if (!d1 && !d2)
         return cudaSuccess;
-    return launch_after(vq_norm_dw_kernel, dim3((H + 31) / 32, 2), dim3(256), 0, s, p1, d1, p2, d2,
-                        T > 0 ? sh.parts : 0, H);
+    return launch_after(vq_norm_dw_kernel, dim3((H + 31) / 32, 2), dim3(256), 0, s, p1, d1, p2, d2, parts, H);
 }
 
-template <typename HT>
-cudaError_t pre_bwd(const NormPreBwdArgs &a, const BwdShape &sh, bool vec8, cudaStream_t s)
+constexpr int PRE_BWD_REGS[4] = {64, 88, 112, 128}, POST_BWD_REGS[4] = {96, 128, 128, 128};
+
+template <auto K, typename Args>
+cudaError_t rows(const NormShape &sh, cudaStream_t s, const Args &a)
 {
-    const dim3 grid(sh.ctas), block(32 * sh.W * sh.R);
-    if (vec8) {
+    return launch_smem<K, NORM_SMEM>(dim3(sh.ctas), dim3(32 * sh.W * sh.R), sh.smem, s, a, sh.S);
+}
+
+// Both launch and say how many partial rows they leave.
+template <typename HT>
+cudaError_t pre_bwd(NormPreBwdArgs a, bool vec8, int &parts, cudaStream_t s)
+{
+    NormShape sh = norm_shape(a.H, a.T, sizeof(HT) * (a.dres ? 2 : 1) + 2, 0, PRE_BWD_REGS, 256, NORM_PARTS);
+    if (vec8 && sh.S > 0) {
+        a.W = sh.W;
+        parts = sh.ctas;
         switch (sh.nv) {
-        case 1: return launch_after(vq_norm_pre_bwd_kernel<HT, 8, 1>, grid, block, 0, s, a);
-        case 2: return launch_after(vq_norm_pre_bwd_kernel<HT, 8, 2>, grid, block, 0, s, a);
-        default: return launch_after(vq_norm_pre_bwd_kernel<HT, 8, 4>, grid, block, 0, s, a);
+        case 1: return rows<vq_norm_pre_bwd_kernel<HT, 1>>(sh, s, a);
+        case 2: return rows<vq_norm_pre_bwd_kernel<HT, 2>>(sh, s, a);
+        case 3: return rows<vq_norm_pre_bwd_kernel<HT, 3>>(sh, s, a);
+        default: return rows<vq_norm_pre_bwd_kernel<HT, 4>>(sh, s, a);
         }
     }
-    switch (sh.nv) {
-    case 1: return launch_after(vq_norm_pre_bwd_kernel<HT, 1, 1>, grid, block, 0, s, a);
-    case 8: return launch_after(vq_norm_pre_bwd_kernel<HT, 1, 8>, grid, block, 0, s, a);
-    default: return launch_after(vq_norm_pre_bwd_kernel<HT, 1, 32>, grid, block, 0, s, a);
-    }
+    sh = scalar_shape(a.H, a.T);
+    a.W = sh.W;
+    parts = sh.ctas * sh.R;
+    const dim3 grid(sh.ctas), block(32 * sh.W * sh.R);
+    return sh.nv == 1   ? launch_after(vq_norm_pre_bwd_scalar_kernel<HT, 1>, grid, block, 0, s, a)
+           : sh.nv == 8 ? launch_after(vq_norm_pre_bwd_scalar_kernel<HT, 8>, grid, block, 0, s, a)
+                        : launch_after(vq_norm_pre_bwd_scalar_kernel<HT, 32>, grid, block, 0, s, a);
 }
 
 template <typename YT, typename HT>
-cudaError_t post_bwd(const NormPostBwdArgs &a, const BwdShape &sh, bool vec8, cudaStream_t s)
+cudaError_t post_bwd(NormPostBwdArgs a, bool vec8, int &parts, cudaStream_t s)
 {
-    const dim3 grid(sh.ctas), block(32 * sh.W * sh.R);
-    if (vec8) {
+    const int gate = a.gate_mode != GATE_CHANNEL ? 0 : a.gate_dtype == VQ_F32 ? 4 : 2;
+    NormShape sh = norm_shape(a.H, a.T, sizeof(YT) + (a.dho ? sizeof(HT) : 0) + (a.next.weight ? sizeof(HT) + 2 : 0) + gate,
+                              (a.post.weight ? 4 : 0) + (a.next.weight ? 4 : 0), POST_BWD_REGS, 512, NORM_PARTS);
+    if (vec8 && sh.S > 0) {
+        a.W = sh.W;
+        parts = sh.ctas;
         switch (sh.nv) {
-        case 1: return launch_after(vq_norm_post_bwd_kernel<YT, HT, 8, 1>, grid, block, 0, s, a);
-        case 2: return launch_after(vq_norm_post_bwd_kernel<YT, HT, 8, 2>, grid, block, 0, s, a);
-        default: return launch_after(vq_norm_post_bwd_kernel<YT, HT, 8, 4>, grid, block, 0, s, a);
+        case 1: return rows<vq_norm_post_bwd_kernel<YT, HT, 1>>(sh, s, a);
+        case 2: return rows<vq_norm_post_bwd_kernel<YT, HT, 2>>(sh, s, a);
+        case 3: return rows<vq_norm_post_bwd_kernel<YT, HT, 3>>(sh, s, a);
+        default: return rows<vq_norm_post_bwd_kernel<YT, HT, 4>>(sh, s, a);
         }
     }
-    switch (sh.nv) {
-    case 1: return launch_after(vq_norm_post_bwd_kernel<YT, HT, 1, 1>, grid, block, 0, s, a);
-    case 8: return launch_after(vq_norm_post_bwd_kernel<YT, HT, 1, 8>, grid, block, 0, s, a);
-    default: return launch_after(vq_norm_post_bwd_kernel<YT, HT, 1, 32>, grid, block, 0, s, a);
-    }
+    sh = scalar_shape(a.H, a.T);
+    a.W = sh.W;
+    parts = sh.ctas * sh.R;
+    const dim3 grid(sh.ctas), block(32 * sh.W * sh.R);
+    return sh.nv == 1   ? launch_after(vq_norm_post_bwd_scalar_kernel<YT, HT, 1>, grid, block, 0, s, a)
+           : sh.nv == 8 ? launch_after(vq_norm_post_bwd_scalar_kernel<YT, HT, 8>, grid, block, 0, s, a)
+                        : launch_after(vq_norm_post_bwd_scalar_kernel<YT, HT, 32>, grid, block, 0, s, a);
 }
 
 }  // namespace
 
 size_t norm_workspace_bytes(int H, int T)
 {
-    // bwd_shape's partial rows: at most NORM_PARTS, and at most 4 (one CTA of one-warp rows) over T
+    // at most NORM_PARTS partial rows of each weight, and at most 3 over T (four one-warp rows in a CTA)
     return (size_t)2 * (size_t)std::min((long)NORM_PARTS, (long)std::max(T, 1) + 3) * (size_t)H * sizeof(float);
 }
 
 cudaError_t launch_norm_pre_bwd(const NormPreBwdArgs &args, int h_dtype, bool vec8, float *dw, float *ws, cudaStream_t s)
 {
     NormPreBwdArgs a = args;
-    const BwdShape sh = bwd_shape(a.H, vec8 ? 8 : 1, a.T);
-    a.W = sh.W;
     a.part = dw ? ws : nullptr;
+    int parts = 0;
     if (a.T > 0) {
-        const cudaError_t e = h_dtype == VQ_F32 ? pre_bwd<float>(a, sh, vec8, s) : pre_bwd<uint16_t>(a, sh, vec8, s);
+        const cudaError_t e = h_dtype == VQ_F32 ? pre_bwd<float>(a, vec8, parts, s) : pre_bwd<uint16_t>(a, vec8, parts, s);
         if (e != cudaSuccess)
             return e;
     }
-    return finish(sh, a.T, a.H, a.part, dw, nullptr, nullptr, s);
+    return finish(parts, a.H, a.part, dw, nullptr, nullptr, s);
 }
 
 cudaError_t launch_norm_post_bwd(const NormPostBwdArgs &args, int y_dtype, int h_dtype, bool vec8, float *dpost,
                                  float *dnext, float *ws, cudaStream_t s)
 {
     NormPostBwdArgs a = args;
-    const BwdShape sh = bwd_shape(a.H, vec8 ? 8 : 1, a.T);
-    a.W = sh.W;
+    // the second half of the workspace holds dnext's partial rows
     a.part1 = dpost ? ws : nullptr;
-    a.part2 = dnext ? ws + (size_t)sh.parts * a.H : nullptr;
+    a.part2 = dnext ? ws + norm_workspace_bytes(a.H, a.T) / (2 * sizeof(float)) : nullptr;
+    int parts = 0;
     if (a.T > 0) {
         cudaError_t e;
         if (y_dtype == VQ_F32)
-            e = h_dtype == VQ_F32 ? post_bwd<float, float>(a, sh, vec8, s) : post_bwd<float, uint16_t>(a, sh, vec8, s);
+            e = h_dtype == VQ_F32 ? post_bwd<float, float>(a, vec8, parts, s) : post_bwd<float, uint16_t>(a, vec8, parts, s);
         else
-            e = h_dtype == VQ_F32 ? post_bwd<uint16_t, float>(a, sh, vec8, s)
-                                  : post_bwd<uint16_t, uint16_t>(a, sh, vec8, s);
+            e = h_dtype == VQ_F32 ? post_bwd<uint16_t, float>(a, vec8, parts, s)
+                                  : post_bwd<uint16_t, uint16_t>(a, vec8, parts, s);
         if (e != cudaSuccess)
             return e;
     }
-    return finish(sh, a.T, a.H, a.part1, dpost, a.part2, dnext, s);
+    return finish(parts, a.H, a.part1, dpost, a.part2, dnext, s);
 }
 
 }  // namespace vq

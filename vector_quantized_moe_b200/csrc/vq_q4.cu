@@ -90,13 +90,6 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t at)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-    return v;
-}
-
 template <int NG>
 __device__ __forceinline__ void lds_pairs(uint32_t at, uint32_t (&v)[NG])
 {
