@@ -57,6 +57,36 @@ cudaError_t launch_smem(dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args
     return e != cudaSuccess ? e : launch_after(K, grid, block, smem, s, args...);
 }
 
+// ---------------------------------------------------------------- pairs
+//
+// Two fp32 operations per instruction (fma.rn.f32x2 and its kin): the row
+// kernels are bound by instruction issue before they are by HBM.
+
+__device__ __forceinline__ uint64_t bits2(float2 v) { return *reinterpret_cast<const uint64_t *>(&v); }
+__device__ __forceinline__ float2 pair2(uint64_t v) { return *reinterpret_cast<const float2 *>(&v); }
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return pair2(d);
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair2(d);
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair2(d);
+}
+
 // ---------------------------------------------------------------- chunks of a row
 //
 // VEC consecutive elements of a row: 8 with 16-byte accesses, or 1.
@@ -88,6 +118,23 @@ struct Chunk<uint16_t, 8> {   // bf16
         r = make_uint4(w[0], w[1], w[2], w[3]);
     }
     __device__ __forceinline__ void store(uint16_t *p) const { *reinterpret_cast<uint4 *>(p) = r; }
+    __device__ __forceinline__ void get(float2 (&v)[4]) const
+    {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
+    __device__ __forceinline__ void set(const float2 (&v)[4])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[i].x, v[i].y);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        r = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 };
 
 template <>
@@ -112,6 +159,16 @@ struct Chunk<float, 8> {
     {
         reinterpret_cast<float4 *>(p)[0] = a;
         reinterpret_cast<float4 *>(p)[1] = b;
+    }
+    __device__ __forceinline__ void get(float2 (&v)[4]) const
+    {
+        v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w);
+        v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
+    }
+    __device__ __forceinline__ void set(const float2 (&v)[4])
+    {
+        a = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        b = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
     }
 };
 
@@ -153,17 +210,24 @@ struct AnyChunk {
         else
             h.get(v);
     }
+    __device__ __forceinline__ void get(float2 (&v)[VEC / 2], int dtype) const
+    {
+        if (dtype == VQ_F32)
+            f.get(v);
+        else
+            h.get(v);
+    }
 };
 
 // A chunk of a norm's weight as fp32, offset added.
-__device__ __forceinline__ void load_weight(const void *p, int dtype, float offset, int c, float (&w)[8])
+__device__ __forceinline__ void load_weight(const void *p, int dtype, float offset, int c, float2 (&w)[4])
 {
     AnyChunk<8> k;
     k.load(p, dtype, c);
     k.get(w, dtype);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        w[j] += offset;
+    for (int j = 0; j < 4; ++j)
+        w[j] = add2(w[j], splat(offset));
 }
 
 // ---------------------------------------------------------------- asynchronous copies
@@ -211,7 +275,7 @@ __device__ __forceinline__ void ring_copy(uint32_t at, uint32_t step, const T *p
 }
 
 template <typename T>
-__device__ __forceinline__ void ring_get(uint32_t at, uint32_t step, float (&v)[8])
+__device__ __forceinline__ void ring_get(uint32_t at, uint32_t step, float2 (&v)[4])
 {
     Chunk<T, 8> c;
     if constexpr (PIECES<T> == 2) {
@@ -224,10 +288,10 @@ __device__ __forceinline__ void ring_get(uint32_t at, uint32_t step, float (&v)[
     c.get(v);
 }
 
-__device__ __forceinline__ void ring_put(uint32_t at, uint32_t step, const float (&v)[8])
+__device__ __forceinline__ void ring_put(uint32_t at, uint32_t step, const float2 (&v)[4])
 {
-    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
-    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + step), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y) : "memory");
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + step), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y) : "memory");
 }
 
 // The same for an array whose type is known at run time.
@@ -239,7 +303,7 @@ __device__ __forceinline__ void ring_copy_any(uint32_t at, uint32_t step, const 
         ring_copy(at, step, static_cast<const uint16_t *>(p) + i);
 }
 
-__device__ __forceinline__ void ring_get_any(uint32_t at, uint32_t step, int dtype, float (&v)[8])
+__device__ __forceinline__ void ring_get_any(uint32_t at, uint32_t step, int dtype, float2 (&v)[4])
 {
     if (dtype == VQ_F32)
         ring_get<float>(at, step, v);
@@ -257,9 +321,27 @@ __device__ __forceinline__ float warp_total(float v)
     return v;
 }
 
-// Sums of N values over the W warps of a row (one row per CTA when W > 1).
-// Two buffers in turn: a warp may start the next sum while another still
-// reads this one.
+// One step of a sum of two values over a warp at once: after it, lanes whose
+// bit `bit` is 0 work on a, the others on b.
+__device__ __forceinline__ float fold(float a, float b, int bit, int lane)
+{
+    const bool up = lane & bit;
+    return (up ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, up ? a : b, bit);
+}
+
+template <int FROM>
+__device__ __forceinline__ float warp_total_from(float v)
+{
+#pragma unroll
+    for (int o = FROM; o; o >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// Sums of N <= 3 values over the W warps of a row (one row per CTA when
+// W > 1), in a fixed order. Several values share the warp's shuffles: 5, 5 and
+// 6 for 1, 2 and 3 values. Two buffers in turn: a warp may start the next sum
+// while another still reads this one.
 template <int N>
 struct RowSum {
     float buf[2][N][32];
@@ -268,21 +350,46 @@ struct RowSum {
 template <int N, int M>
 __device__ __forceinline__ void row_sum(float (&v)[N], RowSum<M> &s, int W, int &turn)
 {
-    static_assert(N <= M, "buffer too small");
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        v[i] = warp_total(v[i]);
-    if (W == 1)
-        return;
+    static_assert(N <= M && N <= 3, "sums");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float x;        // lanes 0, 16, 8: totals of v[0], v[1], v[2]
+    if constexpr (N == 1)
+        x = warp_total_from<16>(v[0]);
+    else if constexpr (N == 2)
+        x = warp_total_from<8>(fold(v[0], v[1], 16, lane));
+    else
+        x = warp_total_from<4>(fold(fold(v[0], v[1], 16, lane), fold(v[2], 0.f, 16, lane), 8, lane));
+    if (W == 1) {
+        v[0] = __shfl_sync(0xFFFFFFFFu, x, 0);
+        if constexpr (N > 1)
+            v[1] = __shfl_sync(0xFFFFFFFFu, x, 16);
+        if constexpr (N > 2)
+            v[2] = __shfl_sync(0xFFFFFFFFu, x, 8);
+        return;
+    }
     if (lane == 0)
+        s.buf[turn][0][warp] = x;
+    if (N > 1 && lane == 16)
+        s.buf[turn][N > 1 ? 1 : 0][warp] = x;
+    if (N > 2 && lane == 8)
+        s.buf[turn][N > 2 ? 2 : 0][warp] = x;
+    __syncthreads();
+    if (W <= 16) {
+        const int l = lane & 15;
+        if constexpr (N == 1) {
+            v[0] = warp_total_from<8>(l < W ? s.buf[turn][0][l] : 0.f);
+        } else {
+            x = warp_total_from<8>(l < W ? s.buf[turn][lane >> 4][l] : 0.f);
+            v[0] = __shfl_sync(0xFFFFFFFFu, x, 0);
+            v[1] = __shfl_sync(0xFFFFFFFFu, x, 16);
+            if constexpr (N > 2)
+                v[2] = warp_total_from<8>(l < W ? s.buf[turn][2][l] : 0.f);
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            s.buf[turn][i][warp] = v[i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        v[i] = warp_total(lane < W ? s.buf[turn][i][lane] : 0.f);
+            v[i] = warp_total_from<16>(lane < W ? s.buf[turn][i][lane] : 0.f);
+    }
     turn ^= 1;
 }
 

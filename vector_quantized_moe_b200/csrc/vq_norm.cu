@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_kernel(const NormPreA
     grid_dep_wait();
     for (int s = 0; s < S - 1; ++s)
         fetch(s);
-    float w[NV][8];
+    float2 w[NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (in[i])
@@ -253,23 +253,24 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_kernel(const NormPreA
         }
         const uint32_t at = base + s * P * step;
         s = s == S - 1 ? 0 : s + 1;
-        float v[NV][8], ss[1] = {0.f};
+        float2 v[NV][4], sq = splat(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (in[i]) {
                 ring_get<HT>(at + i * PH * step, step, v[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
+                for (int j = 0; j < 4; ++j)
+                    sq = fma2(v[i][j], v[i][j], sq);
             }
+        float ss[1] = {sq.x + sq.y};
         row_sum(ss, rs, W, turn);
         const float r = rsqrtf(ss[0] * a.inv_h + a.n.eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (in[i]) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[i][j] = v[i][j] * r * w[i][j];
+                for (int j = 0; j < 4; ++j)
+                    v[i][j] = mul2(mul2(v[i][j], splat(r)), w[i][j]);
                 Chunk<uint16_t, 8> o;
                 o.set(v[i]);
                 o.store(x + i * hop);
@@ -322,12 +323,12 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_kernel(const NormPos
     grid_dep_wait();
     for (int s = 0; s < S - 1; ++s)
         fetch(s);
-    float w1[NV][8], w2[NV][8];
+    float2 w1[NV][4], w2[NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            w1[i][j] = w2[i][j] = 1.f;
+        for (int j = 0; j < 4; ++j)
+            w1[i][j] = w2[i][j] = splat(1.f);
         if (in[i]) {
             if (post)
                 load_weight(a.post.weight, a.post.dtype, a.post.offset, chunk_at<8>(i, tid, W), w1[i]);
@@ -354,53 +355,55 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_kernel(const NormPos
         }
         const uint32_t at = base + s * P * step;
         s = s == S - 1 ? 0 : s + 1;
-        float u[NV][8], ss[1] = {0.f};
+        float2 u[NV][4], sq = splat(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (in[i]) {
                 ring_get<YT>(at + i * PY * step, step, u[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    ss[0] = fmaf(u[i][j], u[i][j], ss[0]);
+                for (int j = 0; j < 4; ++j)
+                    sq = fma2(u[i][j], u[i][j], sq);
             }
         if (post) {
+            float ss[1] = {sq.x + sq.y};
             row_sum(ss, rs, W, turn);
             f *= rsqrtf(ss[0] * a.inv_h + a.post.eps);
         }
-        ss[0] = 0.f;
+        sq = splat(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (in[i]) {
-                float v[8];
+                float2 v[4];
                 ring_get<HT>(at + (OH + i * PH) * step, step, v);
                 if (pz) {
-                    float z[8];
+                    float2 z[4];
                     ring_get_any(at + (OZ + i * pz) * step, step, a.gate_dtype, z);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        u[i][j] *= sigmoid(z[j]);
+                    for (int j = 0; j < 4; ++j)
+                        u[i][j] = mul2(u[i][j], make_float2(sigmoid(z[j].x), sigmoid(z[j].y)));
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] = fmaf(u[i][j] * f, w1[i][j], a.res_scale * v[j]);
+                for (int j = 0; j < 4; ++j)
+                    v[j] = fma2(mul2(u[i][j], splat(f)), w1[i][j], mul2(v[j], splat(a.res_scale)));
                 Chunk<HT, 8> o;
                 o.set(v);   // the row as stored: what the next norm sees
                 o.store(ho + i * hop);
                 o.get(u[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    ss[0] = fmaf(u[i][j], u[i][j], ss[0]);
+                for (int j = 0; j < 4; ++j)
+                    sq = fma2(u[i][j], u[i][j], sq);
             }
         ho += stride * a.ho_ld;
         if (next) {
+            float ss[1] = {sq.x + sq.y};
             row_sum(ss, rs, W, turn);
             const float r2 = rsqrtf(ss[0] * a.inv_h + a.next.eps);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (in[i]) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        u[i][j] = u[i][j] * r2 * w2[i][j];
+                    for (int j = 0; j < 4; ++j)
+                        u[i][j] = mul2(mul2(u[i][j], splat(r2)), w2[i][j]);
                     Chunk<uint16_t, 8> o;
                     o.set(u[i]);
                     o.store(x + i * hop);

@@ -311,14 +311,14 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_scalar_kernel(co
 
 // A CTA's weight gradient: its side-by-side rows' sums added in order into one partial row.
 template <int NV>
-__device__ __forceinline__ void write_part(float *part, const float (&acc)[NV][8], float *side, int tid, int W, int H)
+__device__ __forceinline__ void write_part(float *part, const float2 (&acc)[NV][4], float *side, int tid, int W, int H)
 {
     const int R = blockDim.x / (32 * W), rg = threadIdx.x / (32 * W);
     if (R > 1) {   // one-warp rows (NV = 1): side is [R][256]
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            side[rg * 256 + tid * 8 + j] = acc[0][j];
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<float2 *>(&side[rg * 256 + tid * 8 + 2 * j]) = acc[0][j];
         __syncthreads();
         for (int c = threadIdx.x; c < H; c += blockDim.x) {
             float v = side[c];
@@ -383,14 +383,14 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_bwd_kernel(const Norm
     grid_dep_wait();
     for (int s = 0; s < S - 1; ++s)
         fetch(s);
-    float acc[NV][8], w[NV][8];
+    float2 acc[NV][4], w[NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         if (in[i])
             load_weight(a.n.weight, a.n.dtype, a.n.offset, chunk_at<8>(i, tid, W), w[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            acc[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j)
+            acc[i][j] = splat(0.f);
     }
     int turn = 0, s = 0;
     for (long row = row0; row < a.T; row += stride) {
@@ -403,38 +403,39 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_bwd_kernel(const Norm
         }
         const uint32_t at = base + s * P * step;
         s = s == S - 1 ? 0 : s + 1;
-        float q[2] = {0.f, 0.f};   // |h|^2, sum g h
+        float2 q0 = splat(0.f), q1 = q0;   // |h|^2, sum g h
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (in[i]) {
-                float v[8], d[8];
+                float2 v[4], d[4];
                 ring_get<HT>(at + i * PH * step, step, v);
                 ring_get<uint16_t>(at + (OX + i) * step, step, d);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    q[0] = fmaf(v[j], v[j], q[0]);
-                    q[1] = fmaf(d[j] * w[i][j], v[j], q[1]);
+                for (int j = 0; j < 4; ++j) {
+                    q0 = fma2(v[j], v[j], q0);
+                    q1 = fma2(mul2(d[j], w[i][j]), v[j], q1);
                 }
             }
+        float q[2] = {q0.x + q0.y, q1.x + q1.y};
         row_sum(q, rs, W, turn);
         const float r = rsqrtf(q[0] * a.inv_h + a.n.eps);
         const float rm = r * (r * (q[1] * a.inv_h));   // r mean(g v^)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (in[i]) {
-                float v[8], d[8], o[8];
+                float2 v[4], d[4], o[4];
                 ring_get<HT>(at + i * PH * step, step, v);
                 ring_get<uint16_t>(at + (OX + i) * step, step, d);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    o[j] = 0.f;
+                for (int j = 0; j < 4; ++j)
+                    o[j] = splat(0.f);
                 if (res)
                     ring_get<HT>(at + (OR + i * PH) * step, step, o);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float n = v[j] * r;
-                    acc[i][j] = fmaf(d[j], n, acc[i][j]);
-                    o[j] += fmaf(-n, rm, r * (d[j] * w[i][j]));   // r (g - v^ mean(g v^))
+                for (int j = 0; j < 4; ++j) {
+                    const float2 n = mul2(v[j], splat(r));
+                    acc[i][j] = fma2(d[j], n, acc[i][j]);
+                    o[j] = add2(o[j], fma2(n, splat(-rm), mul2(mul2(d[j], w[i][j]), splat(r))));   // r (g - v^ mean(g v^))
                 }
                 Chunk<HT, 8> oc;
                 oc.set(o);
@@ -504,10 +505,10 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
     grid_dep_wait();
     for (int s = 0; s < S - 1; ++s)
         fetch(s);
-    float acc1[NV][8], acc2[NV][8];
+    float2 acc1[NV][4], acc2[NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        float w[8];
+        float2 w[4];
         if (in[i] && post) {
             load_weight(a.post.weight, a.post.dtype, a.post.offset, chunk_at<8>(i, tid, W), w);
             ring_put(at1 + 2 * i * step, step, w);
@@ -517,8 +518,8 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
             ring_put(at2 + 2 * i * step, step, w);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            acc1[i][j] = acc2[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j)
+            acc1[i][j] = acc2[i][j] = splat(0.f);
     }
     int turn = 0, s = 0;
     for (long row = row0; row < a.T; row += stride) {
@@ -540,81 +541,82 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
         const uint32_t at = base + s * P * step;
         s = s == S - 1 ? 0 : s + 1;
         // the sums that need nothing but the inputs: |h'|^2, sum g h' of the next norm, |y|^2
-        float q[3] = {0.f, 0.f, 0.f};
+        float2 q0 = splat(0.f), q1 = q0, q2 = q0;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (in[i]) {
-                float v[8], d[8], w[8];
+                float2 v[4], d[4], w[4];
                 if (next) {
                     ring_get<HT>(at + (OH + i * PH) * step, step, v);
                     ring_get<uint16_t>(at + (OX + i) * step, step, d);
                     ring_get<float>(at2 + 2 * i * step, step, w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        q[0] = fmaf(v[j], v[j], q[0]);
-                        q[1] = fmaf(d[j] * w[j], v[j], q[1]);
+                    for (int j = 0; j < 4; ++j) {
+                        q0 = fma2(v[j], v[j], q0);
+                        q1 = fma2(mul2(d[j], w[j]), v[j], q1);
                     }
                 }
                 if (post) {
                     ring_get<YT>(at + i * PY * step, step, v);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        q[2] = fmaf(v[j], v[j], q[2]);
+                    for (int j = 0; j < 4; ++j)
+                        q2 = fma2(v[j], v[j], q2);
                 }
             }
+        float q[3] = {q0.x + q0.y, q1.x + q1.y, q2.x + q2.y};
         if (next || post)
             row_sum(q, rs, W, turn);
         const float r2 = rsqrtf(q[0] * a.inv_h + a.next.eps), rm2 = r2 * (r2 * (q[1] * a.inv_h));
         const float r1 = post ? rsqrtf(q[2] * a.inv_h + a.post.eps) : 1.f;
-        const float f = a.out_scale * on;   // du = f dH but for a channel's gate
-        float dH[NV][8], t[2] = {0.f, 0.f};   // sums: g y of the post norm, du u
+        float2 dH[NV][4], t0 = splat(0.f);   // t0: sum g y of the post norm (channel gates), or sum dv u
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (in[i]) {
-                float v[8], w[8];
+                float2 v[4], w[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    dH[i][j] = 0.f;
+                for (int j = 0; j < 4; ++j)
+                    dH[i][j] = splat(0.f);
                 if (has)
                     ring_get<HT>(at + (OG + i * PH) * step, step, dH[i]);
                 if (next) {
-                    float d[8];
+                    float2 d[4];
                     ring_get<HT>(at + (OH + i * PH) * step, step, v);
                     ring_get<uint16_t>(at + (OX + i) * step, step, d);
                     ring_get<float>(at2 + 2 * i * step, step, w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float n = v[j] * r2;
-                        acc2[i][j] = fmaf(d[j], n, acc2[i][j]);
-                        dH[i][j] += fmaf(-n, rm2, r2 * (d[j] * w[j]));
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 n = mul2(v[j], splat(r2));
+                        acc2[i][j] = fma2(d[j], n, acc2[i][j]);
+                        dH[i][j] = add2(dH[i][j], fma2(n, splat(-rm2), mul2(mul2(d[j], w[j]), splat(r2))));
                     }
                 }
                 if (a.dh) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[j] = a.res_scale * dH[i][j];
+                    for (int j = 0; j < 4; ++j)
+                        v[j] = mul2(dH[i][j], splat(a.res_scale));
                     Chunk<HT, 8> oc;
                     oc.set(v);
                     oc.store(dh + i * hop);
                 }
                 ring_get<YT>(at + i * PY * step, step, v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    w[j] = 1.f;
+                for (int j = 0; j < 4; ++j)
+                    w[j] = splat(1.f);
                 if (post)
                     ring_get<float>(at1 + 2 * i * step, step, w);
                 if (pz) {
-                    float z[8];
+                    float2 z[4];
                     ring_get_any(at + (OZ + i * pz) * step, step, a.gate_dtype, z);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float zon, zoff;
-                        sigmoids(z[j], zon, zoff);
-                        const float du = f * dH[i][j] * zon, n = v[j] * r1;
-                        z[j] = du * zoff * (n * w[j]);   // dv u s (1 - s)
-                        acc1[i][j] = fmaf(du, n, acc1[i][j]);
-                        dH[i][j] = du * w[j];            // g
-                        t[0] = fmaf(dH[i][j], v[j], t[0]);
+                    for (int j = 0; j < 4; ++j) {
+                        float2 zon, zoff;
+                        sigmoids(z[j].x, zon.x, zoff.x);
+                        sigmoids(z[j].y, zon.y, zoff.y);
+                        const float2 du = mul2(mul2(dH[i][j], splat(a.out_scale)), zon), n = mul2(v[j], splat(r1));
+                        dH[i][j] = mul2(du, w[j]);                              // g
+                        z[j] = mul2(mul2(dH[i][j], n), zoff);                   // dv u s (1 - s)
+                        acc1[i][j] = fma2(du, n, acc1[i][j]);
+                        t0 = fma2(dH[i][j], v[j], t0);
                     }
                     if (a.dgate) {
                         const long to = row * a.dgate_ld + tid * 8 + i * hop;
@@ -630,21 +632,22 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float du = a.out_scale * dH[i][j], n = v[j] * r1;   // dv
-                        acc1[i][j] = fmaf(du * on, n, acc1[i][j]);
-                        const float dn = du * w[j];
-                        t[1] = fmaf(dn, n, t[1]);                                 // dv u
-                        dH[i][j] = dn * on;                                       // g
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 du = mul2(dH[i][j], splat(a.out_scale)), n = mul2(v[j], splat(r1));   // dv
+                        acc1[i][j] = fma2(mul2(du, splat(on)), n, acc1[i][j]);
+                        const float2 dn = mul2(du, w[j]);
+                        t0 = fma2(dn, n, t0);                                   // dv u
+                        dH[i][j] = mul2(dn, splat(on));                         // g
                     }
                 }
             }
         dh += stride * a.dh_ld;
         const bool token = a.gate_mode == GATE_TOKEN && a.dgate;
+        float t[1] = {t0.x + t0.y};
         if (post || token)
             row_sum(t, rs, W, turn);
         if (token && tid == 0) {
-            const float dz = t[1] * on * off;
+            const float dz = t[0] * on * off;
             const long to = row * a.dgate_ld;
             if (a.gate_dtype == VQ_F32)
                 static_cast<float *>(a.dgate)[to] = dz;
@@ -652,16 +655,16 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
                 static_cast<uint16_t *>(a.dgate)[to] = f32_to_bf16_bits(dz);
         }
         // r1 mean(g y^): from sum g y, or from sum dv u = sum (g / on) y^
-        const float rm1 = r1 * ((pz ? r1 * t[0] : on * t[1]) * a.inv_h);
+        const float rm1 = r1 * ((pz ? r1 : on) * t[0] * a.inv_h);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (in[i]) {
                 if (post) {
-                    float v[8];
+                    float2 v[4];
                     ring_get<YT>(at + i * PY * step, step, v);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        dH[i][j] = fmaf(-(v[j] * r1), rm1, r1 * dH[i][j]);
+                    for (int j = 0; j < 4; ++j)
+                        dH[i][j] = fma2(mul2(v[j], splat(r1)), splat(-rm1), mul2(dH[i][j], splat(r1)));
                 }
                 Chunk<YT, 8> oc;
                 oc.set(dH[i]);
