@@ -183,8 +183,14 @@ def live_rank(live_bitmap: np.ndarray, rows: int) -> np.ndarray:
 # ------------------------------------------------------------------ device side
 
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_torch_module = None
 
 
 def _stream(stream=None) -> int:
@@ -332,88 +338,73 @@ def fit_check(workspace, stream=None) -> int:
 # norm -> (router) -> experts and 4-bit shared expert -> gate, norm, residual, next norm, and the router's balance
 # loss. bf16 arrays may be torch.bfloat16 or their int16 bit patterns; outputs are torch.bfloat16. Rows may be
 # windows of wider arrays (a row stride), with consecutive elements inside a row. Every call checks its tensors
-# (VQError with VQ_ERR_ARG) before it launches, runs on its tensors' device, and on `stream` when one is given (the
-# outputs then belong to that stream).
+# (VQError with VQ_ERR_ARG) before it launches and runs on its tensors' device: on that device's current stream, or on
+# `stream` when one is given (the outputs then belong to that stream).
 
-def _device_call(f):
-    """Runs f on the device of its tensors and on the `stream` argument, if any."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        torch = _torch()
-        if stream is None:
-            dev = _device_of((*args, *kw.values()) if kw else args)
-            if dev is None or dev == torch._C._cuda_getDevice():
-                return f(*args, **kw)
-            with torch.cuda.device(dev):
-                return f(*args, **kw)
-        with torch.cuda.stream(stream):
-            out = f(*args, **kw)
-        for t in (*args, *kw.values()):
-            if isinstance(t, torch.Tensor) and t.is_cuda:
-                t.record_stream(stream)
-        return out
-    return call
+_bf16 = _f32 = _codes = _device = _raw_stream = None
 
 
-def _device_of(args):
-    """CUDA device index of the first tensor (or weight) among args; None when that is not on a GPU."""
-    Tensor = _torch().Tensor
-    for a in args:
-        if isinstance(a, Tensor):
-            return a.get_device() if a.is_cuda else None
-    return None
-
-
-def _raw_stream(dev: int) -> int:
-    return _torch()._C._cuda_getCurrentRawStream(dev)
+def _types():
+    """Binds what the calls below use of torch once (they are on a decode step's host path)."""
+    global _bf16, _f32, _codes, _device, _raw_stream
+    torch = _torch()
+    _bf16, _f32 = torch.bfloat16, torch.float32
+    _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _codes = {torch.float32: VQ_F32, torch.bfloat16: VQ_BF16, torch.int16: VQ_BF16}
 
 
 def _bad(where: str):
     raise VQError(VQ_ERR_ARG, where)
 
 
-_dtype_codes = None
+def _on_stream(stream, f, *args):
+    """f(*args) with `stream` current: its outputs are allocated on it, its inputs are held until it has run."""
+    torch = _torch()
+    with torch.cuda.stream(stream):
+        out = f(*args)
+    for t in args:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    return out
 
 
-def _dtype_code(dtype):
-    """VQ_F32 or VQ_BF16 of a tensor type, None for any other."""
-    global _dtype_codes
-    if _dtype_codes is None:
-        torch = _torch()
-        _dtype_codes = {torch.float32: VQ_F32, torch.bfloat16: VQ_BF16, torch.int16: VQ_BF16}
-    return _dtype_codes.get(dtype)
+def _launch(name, dev, *args):
+    """Calls the library on device `dev` and its current stream."""
+    fn = getattr(_lib_handle, name)
+    if dev == _device():
+        st = fn(*args, _raw_stream(dev))
+    else:
+        with _torch().cuda.device(dev):
+            st = fn(*args, _raw_stream(dev))
+    if st != VQ_OK:
+        raise VQError(st, name)
 
 
 def _row_arg(where, t, T, cols, like=None):
     """(pointer, dtype, row stride) of a [T, cols] array; VQError when t is not one. like: its required dtype code."""
-    if t is None:
-        return None, VQ_F32, 0
-    code = _dtype_code(t.dtype)
-    if code is None or (like is not None and code != like) or t.dim() != 2:
+    code = _codes.get(t.dtype)
+    if code is None or (like is not None and code != like) or t.shape != (T, cols):
         _bad(where)
-    shape, stride = t.shape, t.stride()
-    if shape[0] != T or shape[1] != cols or (cols > 1 and stride[1] != 1) or (T > 1 and stride[0] < cols):
+    ld, inner = t.stride()
+    if (cols > 1 and inner != 1) or (T > 1 and ld < cols):
         _bad(where)
-    return t.data_ptr(), code, stride[0]
+    return t.data_ptr(), code, ld
 
 
-def _same_device(where, *tensors) -> int:
-    """Index of the one GPU that all tensors (None: skipped) are on, which is the current device."""
-    dev = -1
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d < 0 or (dev >= 0 and d != dev):
-                _bad(where + " (tensors on different devices, or not on a GPU)")
-            dev = d
-    if dev != _torch()._C._cuda_getDevice():
-        _bad(where + " (stream of another device)")
+def _one_device(where, first, *others) -> int:
+    """Index of the one GPU that all tensors (None: skipped) are on."""
+    dev = first.get_device()
+    if dev < 0:
+        _bad(where + " (not on a GPU)")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            _bad(where + " (tensors on different devices)")
     return dev
 
 
-def _empty_ws(n, workspace, dev):
-    """(tensor, aligned pointer, bytes) of a workspace of n bytes: the given one, or a new one."""
-    ws = workspace if workspace is not None else _torch().empty(n + 256, dtype=_torch().uint8, device=dev)
+def _workspace(n, given, like):
+    """(tensor, aligned pointer, bytes) of a workspace of n bytes: the given one, or a new one on like's device."""
+    ws = given if given is not None else like.new_empty(n + 256, dtype=_torch().uint8)
     base = ws.data_ptr()
     aligned = (base + 255) // 256 * 256
     return ws, aligned, ws.numel() * ws.element_size() - (aligned - base)
@@ -424,7 +415,10 @@ class Norm:
     store weight - 1."""
 
     def __init__(self, weight, eps: float = 1e-6, offset: float = 0.0):
-        code = _dtype_code(weight.dtype)
+        if _codes is None:
+            _types()
+        _L()
+        code = _codes.get(weight.dtype)
         if code is None or weight.dim() != 1 or weight.numel() < 1 or not weight.is_contiguous():
             _bad("Norm: weight")
         self.weight, self.hidden = weight, weight.numel()
@@ -432,17 +426,27 @@ class Norm:
         self._ref = ctypes.byref(self._s)
 
 
-@_device_call
-def norm_pre(norm: Norm, h, out=None):
+def norm_pre(norm: Norm, h, out=None, stream=None):
     """x [T, hidden] bf16 = norm(h), the input of a block from the residual stream h (fp32 or bf16) (vq_norm_pre)."""
-    T, H = h.shape[0], norm.hidden
+    if stream is not None:
+        return _on_stream(stream, norm_pre, norm, h, out)
+    T, H = len(h), norm.hidden
     hp, hd, hl = _row_arg("norm_pre: h", h, T, H)
     if out is None:
-        out = _torch().empty((T, H), dtype=_torch().bfloat16, device=h.device)
-    xp, _, xl = _row_arg("norm_pre: out", out, T, H, VQ_BF16)
-    dev = _same_device("norm_pre", h, norm.weight, out)
-    _check(_L().vq_norm_pre(norm._ref, hp, hd, hl, T, xp, xl, _raw_stream(dev)), "vq_norm_pre")
+        out = _empty(h, _bf16)
+        xp, xl = out.data_ptr(), H
+    else:
+        xp, _, xl = _row_arg("norm_pre: out", out, T, H, VQ_BF16)
+    dev = _one_device("norm_pre", h, norm.weight, out)
+    _launch("vq_norm_pre", dev, norm._ref, hp, hd, hl, T, xp, xl)
     return out
+
+
+def _empty(like, dtype):
+    """A new contiguous array of like's shape on its device."""
+    if like.dtype is dtype:
+        return _torch().empty_like(like)
+    return like.new_empty(like.shape, dtype=dtype)
 
 
 @functools.lru_cache(maxsize=None)
@@ -450,118 +454,149 @@ def _norm_ws(H, T):
     return int(_L().vq_norm_workspace_size(H, T))
 
 
-@_device_call
-def norm_pre_backward(norm: Norm, h, dx, dres=None, weight_grad: bool = True, workspace=None):
+def norm_pre_backward(norm: Norm, h, dx, dres=None, weight_grad: bool = True, workspace=None, stream=None):
     """(dh, dweight fp32 or None) of norm_pre for the gradient dx (bf16); dres: a gradient that reaches h past the
     norm, added to dh (vq_norm_pre_backward)."""
-    torch = _torch()
-    T, H = h.shape[0], norm.hidden
+    if stream is not None:
+        return _on_stream(stream, norm_pre_backward, norm, h, dx, dres, weight_grad, workspace)
+    T, H = len(h), norm.hidden
     hp, hd, hl = _row_arg("norm_pre_backward: h", h, T, H)
     xp, _, xl = _row_arg("norm_pre_backward: dx", dx, T, H, VQ_BF16)
-    rp, _, rl = _row_arg("norm_pre_backward: dres", dres, T, H, hd)
-    dh = torch.empty((T, H), dtype=torch.float32 if hd == VQ_F32 else torch.bfloat16, device=h.device)
-    dev = _same_device("norm_pre_backward", h, norm.weight, dx, dres, workspace)
-    dw = wp = None
+    rp, rl = None, 0
+    if dres is not None:
+        rp, _, rl = _row_arg("norm_pre_backward: dres", dres, T, H, hd)
+    dev = _one_device("norm_pre_backward", h, norm.weight, dx, dres, workspace)
+    dh = _empty(h, _f32 if hd == VQ_F32 else _bf16)
+    dw = wp = dp = None
     nb = 0
     if weight_grad:
-        dw = torch.empty(H, dtype=torch.float32, device=h.device)
-        workspace, wp, nb = _empty_ws(_norm_ws(H, T), workspace, h.device)
-    _check(_L().vq_norm_pre_backward(norm._ref, hp, hd, hl, xp, xl, rp, rl, T, dh.data_ptr(), H, _ptr(dw), wp, nb,
-                                     _raw_stream(dev)), "vq_norm_pre_backward")
+        dw = h.new_empty(H, dtype=_f32)
+        dp = dw.data_ptr()
+        workspace, wp, nb = _workspace(_norm_ws(H, T), workspace, h)
+    _launch("vq_norm_pre_backward", dev, norm._ref, hp, hd, hl, xp, xl, rp, rl, T, dh.data_ptr(), H, dp, wp, nb)
     return dh, dw
 
 
 def _gate_arg(where, gate, T, H):
     """(pointer, dtype, columns, row stride) of gate logits [T], [T, 1] or [T, H]."""
-    if gate is None:
-        return None, VQ_F32, 0, 0
-    cols = 1 if gate.dim() == 1 else gate.shape[1] if gate.dim() == 2 else 0
+    shape = gate.shape
+    if len(shape) == 1:
+        gate = gate.unsqueeze(1)
+        cols = 1
+    else:
+        cols = shape[1] if len(shape) == 2 else 0
     if cols != 1 and cols != H:
         _bad(where)
-    p, d, ld = _row_arg(where, gate.unsqueeze(1) if gate.dim() == 1 else gate, T, cols)
+    p, d, ld = _row_arg(where, gate, T, cols)
     return p, d, cols, ld
 
 
 def _norm_ref(where, norm, H):
-    if norm is None:
-        return None
     if norm.hidden != H:
         _bad(where)
     return norm._ref
 
 
-@_device_call
 def norm_post(y, h, post: Optional[Norm] = None, gate=None, res_scale: float = 1.0, out_scale: float = 1.0,
-              next: Optional[Norm] = None, h_out=None, x_out=None):
+              next: Optional[Norm] = None, h_out=None, x_out=None, stream=None):
     """(h_out, x_out) of a block whose output is y [T, hidden] and whose residual stream is h:
     h_out = res_scale * h + out_scale * sigmoid(gate) * post(y) and x_out = next(h_out) in bf16 (None without next).
     gate: logits [T], [T, 1] or [T, hidden]. h_out may be h (vq_norm_post)."""
-    torch = _torch()
-    T, H = y.shape if y.dim() == 2 else _bad("norm_post: y")
+    if stream is not None:
+        return _on_stream(stream, norm_post, y, h, post, gate, res_scale, out_scale, next, h_out, x_out)
+    if _codes is None:
+        _types()
+        _L()
+    if y.dim() != 2:
+        _bad("norm_post: y")
+    T, H = y.shape
     yp, yd, yl = _row_arg("norm_post: y", y, T, H)
     hp, hd, hl = _row_arg("norm_post: h", h, T, H)
-    gp, gd, gc, gl = _gate_arg("norm_post: gate", gate, T, H)
-    pr, nr = _norm_ref("norm_post: post", post, H), _norm_ref("norm_post: next", next, H)
-    if x_out is not None and next is None:
+    gp = pr = nr = xp = w1 = w2 = None
+    gd = gc = gl = xl = 0
+    if gate is not None:
+        gp, gd, gc, gl = _gate_arg("norm_post: gate", gate, T, H)
+    if post is not None:
+        pr, w1 = _norm_ref("norm_post: post", post, H), post.weight
+    if next is not None:
+        nr, w2 = _norm_ref("norm_post: next", next, H), next.weight
+        if x_out is None:
+            x_out = _empty(h, _bf16)
+            xp, xl = x_out.data_ptr(), H
+        else:
+            xp, _, xl = _row_arg("norm_post: x_out", x_out, T, H, VQ_BF16)
+    elif x_out is not None:
         _bad("norm_post: x_out without next")
     if h_out is None:
-        h_out = torch.empty((T, H), dtype=torch.float32 if hd == VQ_F32 else torch.bfloat16, device=y.device)
-    if x_out is None and next is not None:
-        x_out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
-    op, _, ol = _row_arg("norm_post: h_out", h_out, T, H, hd)
-    xp, _, xl = _row_arg("norm_post: x_out", x_out, T, H, VQ_BF16)
-    dev = _same_device("norm_post", y, h, gate, h_out, x_out, None if post is None else post.weight,
-                       None if next is None else next.weight)
-    _check(_L().vq_norm_post(pr, nr, H, yp, yd, yl, gp, gd, gc, gl, hp, hd, hl, res_scale, out_scale, T, op, ol, xp, xl,
-                             _raw_stream(dev)), "vq_norm_post")
+        h_out = _empty(h, _f32 if hd == VQ_F32 else _bf16)
+        op, ol = h_out.data_ptr(), H
+    else:
+        op, _, ol = _row_arg("norm_post: h_out", h_out, T, H, hd)
+    dev = _one_device("norm_post", y, h, gate, h_out, x_out, w1, w2)
+    _launch("vq_norm_post", dev, pr, nr, H, yp, yd, yl, gp, gd, gc, gl, hp, hd, hl, res_scale, out_scale, T, op, ol, xp, xl)
     return h_out, x_out
 
 
-@_device_call
 def norm_post_backward(y, h_out, dh_out, dx_out=None, post: Optional[Norm] = None, gate=None, res_scale: float = 1.0,
-                       out_scale: float = 1.0, next: Optional[Norm] = None, workspace=None):
+                       out_scale: float = 1.0, next: Optional[Norm] = None, workspace=None, stream=None):
     """(dy, dgate, dh, dpost, dnext) of norm_post from its y, gate and h_out and the gradients dh_out (may be None: 0)
     and dx_out (with next). Gradients of bf16 arrays are bf16, dpost and dnext fp32; None for what the call did not
     have (vq_norm_post_backward)."""
-    torch = _torch()
-    T, H = y.shape if y.dim() == 2 else _bad("norm_post_backward: y")
+    if stream is not None:
+        return _on_stream(stream, norm_post_backward, y, h_out, dh_out, dx_out, post, gate, res_scale, out_scale, next,
+                          workspace)
+    if _codes is None:
+        _types()
+        _L()
+    if y.dim() != 2:
+        _bad("norm_post_backward: y")
+    T, H = y.shape
     yp, yd, yl = _row_arg("norm_post_backward: y", y, T, H)
     hp, hd, hl = _row_arg("norm_post_backward: h_out", h_out, T, H)
-    gp, gd, gc, gl = _gate_arg("norm_post_backward: gate", gate, T, H)
-    ap, _, al = _row_arg("norm_post_backward: dh_out", dh_out, T, H, hd)
-    xp, _, xl = _row_arg("norm_post_backward: dx_out", dx_out, T, H, VQ_BF16)
-    pr = _norm_ref("norm_post_backward: post", post, H)
-    nr = _norm_ref("norm_post_backward: next", next, H)
     if (dx_out is None) != (next is None):
         _bad("norm_post_backward: dx_out goes with next")
-    dev = _same_device("norm_post_backward", y, h_out, gate, dh_out, dx_out, workspace,
-                       None if post is None else post.weight, None if next is None else next.weight)
-    like = lambda code: torch.float32 if code == VQ_F32 else torch.bfloat16  # noqa: E731
-    dy = torch.empty((T, H), dtype=like(yd), device=y.device)
-    dh = torch.empty((T, H), dtype=like(hd), device=y.device)
-    dgate = None if gate is None else torch.empty(gate.shape, dtype=like(gd), device=y.device)
-    dpost = None if post is None else torch.empty(H, dtype=torch.float32, device=y.device)
-    dnext = None if next is None else torch.empty(H, dtype=torch.float32, device=y.device)
-    wp, nb = None, 0
+    ap = xp = gp = pr = nr = wp = w1 = w2 = dgate = dpost = dnext = zp = d1 = d2 = None
+    al = xl = gd = gc = gl = nb = 0
+    if dh_out is not None:
+        ap, _, al = _row_arg("norm_post_backward: dh_out", dh_out, T, H, hd)
+    if gate is not None:
+        gp, gd, gc, gl = _gate_arg("norm_post_backward: gate", gate, T, H)
+    if post is not None:
+        pr, w1 = _norm_ref("norm_post_backward: post", post, H), post.weight
+    if next is not None:
+        nr, w2 = _norm_ref("norm_post_backward: next", next, H), next.weight
+        xp, _, xl = _row_arg("norm_post_backward: dx_out", dx_out, T, H, VQ_BF16)
+    dev = _one_device("norm_post_backward", y, h_out, gate, dh_out, dx_out, workspace, w1, w2)
+    dy = _empty(y, _f32 if yd == VQ_F32 else _bf16)
+    dh = _empty(h_out, _f32 if hd == VQ_F32 else _bf16)
+    if gate is not None:
+        dgate = gate.new_empty(gate.shape, dtype=_f32 if gd == VQ_F32 else _bf16)
+        zp = dgate.data_ptr()
+    if post is not None:
+        dpost = y.new_empty(H, dtype=_f32)
+        d1 = dpost.data_ptr()
+    if next is not None:
+        dnext = y.new_empty(H, dtype=_f32)
+        d2 = dnext.data_ptr()
     if post is not None or next is not None:
-        workspace, wp, nb = _empty_ws(_norm_ws(H, T), workspace, y.device)
-    _check(_L().vq_norm_post_backward(pr, nr, H, yp, yd, yl, gp, gd, gc, gl, hp, hd, hl, res_scale, out_scale, T, ap, al,
-                                      xp, xl, dy.data_ptr(), H, _ptr(dgate), gc, dh.data_ptr(), H, _ptr(dpost),
-                                      _ptr(dnext), wp, nb, _raw_stream(dev)), "vq_norm_post_backward")
+        workspace, wp, nb = _workspace(_norm_ws(H, T), workspace, y)
+    _launch("vq_norm_post_backward", dev, pr, nr, H, yp, yd, yl, gp, gd, gc, gl, hp, hd, hl, res_scale, out_scale, T, ap,
+            al, xp, xl, dy.data_ptr(), H, zp, gc, dh.data_ptr(), H, d1, d2, wp, nb)
     return dy, dgate, dh, dpost, dnext
 
 
 def _mask_arg(where, mask, T):
-    if mask is None:
-        return None
-    if mask.dtype not in (_torch().bool, _torch().uint8) or mask.dim() != 1 or mask.shape[0] != T or \
-            not mask.is_contiguous():
+    torch = _torch()
+    if mask.dtype not in (torch.bool, torch.uint8) or mask.shape != (T,) or not mask.is_contiguous():
         _bad(where)
     return mask.data_ptr()
 
 
 def _logits_arg(where, logits):
-    if logits.dtype != _torch().float32 or logits.dim() != 2 or not logits.is_contiguous():
+    if _codes is None:
+        _types()
+        _L()
+    if logits.dtype is not _f32 or logits.dim() != 2 or not logits.is_contiguous():
         _bad(where)
     return logits.shape
 
@@ -571,41 +606,43 @@ def _balance_ws(T, E):
     return int(_L().vq_balance_workspace_size(T, E))
 
 
-@_device_call
-def balance_loss(logits, ids, mask=None, coef: float = 1.0, workspace=None):
+def balance_loss(logits, ids, mask=None, coef: float = 1.0, workspace=None, stream=None):
     """(loss fp32 scalar, counts int32 [E + 1], probs fp32 [E]) of router logits [T, E] (fp32) and the ids [T, k]
     that route() chose: counts[e] pairs go to expert e, counts[E] tokens count (mask, bool or bytes [T], leaves others
     out), probs is the mean softmax, loss = coef * sum_e (E counts[e] / (counts[E] k)) probs[e] (vq_balance_loss)."""
+    if stream is not None:
+        return _on_stream(stream, balance_loss, logits, ids, mask, coef, workspace)
     torch = _torch()
     T, E = _logits_arg("balance_loss: logits", logits)
-    if ids.dtype != torch.int32 or ids.dim() != 2 or ids.shape[0] != T or not ids.is_contiguous():
+    if ids.dtype is not torch.int32 or ids.dim() != 2 or len(ids) != T or not ids.is_contiguous():
         _bad("balance_loss: ids")
-    mp = _mask_arg("balance_loss: mask", mask, T)
-    dev = _same_device("balance_loss", logits, ids, mask, workspace)
-    loss = torch.empty((), dtype=torch.float32, device=logits.device)
-    counts = torch.empty(E + 1, dtype=torch.int32, device=logits.device)
-    probs = torch.empty(E, dtype=torch.float32, device=logits.device)
-    workspace, wp, nb = _empty_ws(_balance_ws(T, E), workspace, logits.device)
-    _check(_L().vq_balance_loss(logits.data_ptr(), ids.data_ptr(), mp, T, E, ids.shape[1], coef, loss.data_ptr(),
-                                counts.data_ptr(), probs.data_ptr(), wp, nb, _raw_stream(dev)), "vq_balance_loss")
+    mp = None if mask is None else _mask_arg("balance_loss: mask", mask, T)
+    dev = _one_device("balance_loss", logits, ids, mask, workspace)
+    loss = logits.new_empty(())
+    probs = logits.new_empty(E)
+    counts = ids.new_empty(E + 1)
+    workspace, wp, nb = _workspace(_balance_ws(T, E), workspace, logits)
+    _launch("vq_balance_loss", dev, logits.data_ptr(), ids.data_ptr(), mp, T, E, ids.shape[1], coef, loss.data_ptr(),
+            counts.data_ptr(), probs.data_ptr(), wp, nb)
     return loss, counts, probs
 
 
-@_device_call
-def balance_loss_backward(logits, counts, top_k: int, dloss=None, mask=None, coef: float = 1.0):
+def balance_loss_backward(logits, counts, top_k: int, dloss=None, mask=None, coef: float = 1.0, stream=None):
     """dlogits fp32 [T, E] of balance_loss, from the counts it gave for the same mask; dloss: fp32 scalar tensor on
     the device, None for 1 (vq_balance_loss_backward)."""
+    if stream is not None:
+        return _on_stream(stream, balance_loss_backward, logits, counts, top_k, dloss, mask, coef)
     torch = _torch()
     T, E = _logits_arg("balance_loss_backward: logits", logits)
-    if counts.dtype != torch.int32 or counts.dim() != 1 or counts.shape[0] != E + 1 or not counts.is_contiguous():
+    if counts.dtype is not torch.int32 or counts.shape != (E + 1,) or not counts.is_contiguous():
         _bad("balance_loss_backward: counts")
-    if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != 1):
+    if dloss is not None and (dloss.dtype is not _f32 or dloss.numel() != 1):
         _bad("balance_loss_backward: dloss")
-    mp = _mask_arg("balance_loss_backward: mask", mask, T)
-    dev = _same_device("balance_loss_backward", logits, counts, mask, dloss)
-    out = torch.empty((T, E), dtype=torch.float32, device=logits.device)
-    _check(_L().vq_balance_loss_backward(logits.data_ptr(), counts.data_ptr(), mp, T, E, top_k, coef, _ptr(dloss),
-                                         out.data_ptr(), _raw_stream(dev)), "vq_balance_loss_backward")
+    mp = None if mask is None else _mask_arg("balance_loss_backward: mask", mask, T)
+    dev = _one_device("balance_loss_backward", logits, counts, mask, dloss)
+    out = torch.empty_like(logits)
+    _launch("vq_balance_loss_backward", dev, logits.data_ptr(), counts.data_ptr(), mp, T, E, top_k, coef,
+            None if dloss is None else dloss.data_ptr(), out.data_ptr())
     return out
 
 
@@ -613,6 +650,9 @@ class Q4Module:
     """A dense 4-bit matrix [rows, cols] with group scales on the device, in the kernel's tile layout (vq_q4_module)."""
 
     def __init__(self, rows, cols, group, words, scales, biases=None):
+        if _codes is None:
+            _types()
+        _L()
         self.rows, self.cols, self.group = rows, cols, group
         self.words, self.scales, self.biases = words, scales, biases
         self._s = vq_q4_module(rows, cols, group, _ptr(words), _ptr(scales), _ptr(biases))
@@ -623,47 +663,46 @@ class Q4Module:
         """Lays row-major device arrays out (vq_q4_pack): words int32 [rows, cols / 8] (pack(codes, 4)'s rows), scales
         and biases fp16 (or their int16 bits) [rows, cols / group]. Without biases W = scale * (q - 8), with them
         W = scale * q + bias."""
-        return _q4_from_rows(words, scales, biases, group, stream=stream)
+        if stream is not None:
+            return _on_stream(stream, cls.from_rows, words, scales, biases, group)
+        torch = _torch()
+        if _codes is None:
+            _types()
+        if words.dtype not in (torch.int32, torch.uint32) or words.dim() != 2 or not words.is_contiguous():
+            _bad("Q4Module.from_rows: words")
+        rows, cols = words.shape[0], words.shape[1] * 8
+        if group not in (32, 64, 128) or cols % group:
+            _bad("Q4Module.from_rows: group")
+        for name, t in (("scales", scales), ("biases", biases)):
+            if t is not None and (t.dtype not in (torch.float16, torch.int16) or t.shape != (rows, cols // group)
+                                  or not t.is_contiguous()):
+                _bad("Q4Module.from_rows: " + name)
+        nw, ns = int(_L().vq_q4_packed_words(rows, cols)), int(_L().vq_q4_packed_scales(rows, cols, group))
+        if nw == 0 or ns == 0:
+            _bad("Q4Module.from_rows")
+        dev = _one_device("Q4Module.from_rows", words, scales, biases)
+        w = words.new_empty(nw, dtype=torch.int32)
+        s = scales.new_empty(ns, dtype=torch.int16)
+        b = None if biases is None else biases.new_empty(ns, dtype=torch.int16)
+        _launch("vq_q4_pack", dev, words.data_ptr(), scales.data_ptr(), _ptr(biases), rows, cols, group, w.data_ptr(),
+                s.data_ptr(), _ptr(b))
+        return cls(rows, cols, group, w, s, b)
 
 
-@_device_call
-def _q4_from_rows(words, scales, biases, group):
-    torch = _torch()
-    if words.dtype not in (torch.int32, torch.uint32) or words.dim() != 2 or not words.is_contiguous():
-        _bad("Q4Module.from_rows: words")
-    rows, cols = words.shape[0], words.shape[1] * 8
-    if group not in (32, 64, 128) or cols % group:
-        _bad("Q4Module.from_rows: group")
-    for name, t in (("scales", scales), ("biases", biases)):
-        if t is not None and (t.dtype not in (torch.float16, torch.int16) or tuple(t.shape) != (rows, cols // group)
-                              or not t.is_contiguous()):
-            _bad("Q4Module.from_rows: " + name)
-    nw, ns = int(_L().vq_q4_packed_words(rows, cols)), int(_L().vq_q4_packed_scales(rows, cols, group))
-    if nw == 0 or ns == 0:
-        _bad("Q4Module.from_rows")
-    dev = _same_device("Q4Module.from_rows", words, scales, biases)
-    w = torch.empty(nw, dtype=torch.int32, device=words.device)
-    s = torch.empty(ns, dtype=torch.int16, device=words.device)
-    b = None if biases is None else torch.empty(ns, dtype=torch.int16, device=words.device)
-    _check(_L().vq_q4_pack(words.data_ptr(), scales.data_ptr(), _ptr(biases), rows, cols, group, w.data_ptr(),
-                           s.data_ptr(), _ptr(b), _raw_stream(dev)), "vq_q4_pack")
-    return Q4Module(rows, cols, group, w, s, b)
-
-
-@_device_call
-def q4_gemv(m: Q4Module, x, up: Optional[Q4Module] = None, out_dtype=None, out=None):
+def q4_gemv(m: Q4Module, x, up: Optional[Q4Module] = None, out_dtype=None, out=None, stream=None):
     """y [T, rows] = x [T, cols] (bf16) . W^T; with up: silu(x . W^T) * (x . W_up^T) (vq_q4_gemv). out_dtype: float32
     or bfloat16 (the default, or out's)."""
-    torch = _torch()
-    T = x.shape[0]
+    if stream is not None:
+        return _on_stream(stream, q4_gemv, m, x, up, out_dtype, out)
+    T, rows = len(x), m.rows
     xp, _, xl = _row_arg("q4_gemv: x", x, T, m.cols, VQ_BF16)
     if out is None:
-        out = torch.empty((T, m.rows), dtype=out_dtype or torch.bfloat16, device=x.device)
+        out = x.new_empty((T, rows), dtype=out_dtype or _bf16)
     elif out_dtype is not None and out.dtype != out_dtype:
         _bad("q4_gemv: out_dtype")
-    yp, yd, yl = _row_arg("q4_gemv: out", out, T, m.rows)
-    dev = _same_device("q4_gemv", x, m.words, None if up is None else up.words, out)
-    _check(_L().vq_q4_gemv(m._ref, None if up is None else up._ref, xp, xl, T, yp, yd, yl, _raw_stream(dev)), "vq_q4_gemv")
+    yp, yd, yl = _row_arg("q4_gemv: out", out, T, rows)
+    dev = _one_device("q4_gemv", x, m.words, out, None if up is None else up.words)
+    _launch("vq_q4_gemv", dev, m._ref, None if up is None else up._ref, xp, xl, T, yp, yd, yl)
     return out
 
 
