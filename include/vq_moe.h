@@ -372,7 +372,8 @@ vq_status vq_norm_post_backward(const vq_norm *post, const vq_norm *next, int32_
                                 int64_t dgate_ld, void *dh, int64_t dh_ld, float *dpost, float *dnext, void *workspace,
                                 size_t ws_bytes, void *stream);
 
-/* Bytes of workspace vq_balance_loss needs; 0 on invalid sizes. */
+/* Bytes of workspace vq_balance_loss needs for T tokens: 0 up to 64 tokens (one CTA does it all; workspace may be NULL),
+ * and on invalid sizes. */
 size_t vq_balance_workspace_size(int32_t T, int32_t E);
 
 /* The router's balance loss and the experts' load, over the tokens that count (mask NULL, or mask[t] != 0; mask:

@@ -90,7 +90,7 @@ def test_norm_post_backward(kw, status):
     assert post_bwd(**kw) == status
 
 
-def loss(logits=4096, ids=8192, mask=None, T=4, E=16, k=2, coef=1.0, loss=16384, counts=20480, probs=24576, ws=1 << 20,
+def loss(logits=4096, ids=8192, mask=None, T=100, E=16, k=2, coef=1.0, loss=16384, counts=20480, probs=24576, ws=1 << 20,
          nws=1 << 30):
     return vq._L().vq_balance_loss(logits, ids, mask, T, E, k, coef, loss, counts, probs, ws, nws, None)
 
@@ -104,6 +104,11 @@ def loss(logits=4096, ids=8192, mask=None, T=4, E=16, k=2, coef=1.0, loss=16384,
 ])
 def test_balance_loss(kw, status):
     assert loss(**kw) == status
+
+
+def test_balance_workspace_size():
+    f = vq._L().vq_balance_workspace_size
+    assert f(64, 512) == 0 and 0 < f(65, 512) == f(1 << 20, 512) and f(65, 4097) == 0 and f(-1, 8) == 0
 
 
 @pytest.mark.parametrize("kw,status", [

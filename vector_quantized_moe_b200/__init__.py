@@ -621,7 +621,9 @@ def balance_loss(logits, ids, mask=None, coef: float = 1.0, workspace=None, stre
     loss = logits.new_empty(())
     probs = logits.new_empty(E)
     counts = ids.new_empty(E + 1)
-    workspace, wp, nb = _workspace(_balance_ws(T, E), workspace, logits)
+    wp, nb = None, _balance_ws(T, E)
+    if nb:
+        workspace, wp, nb = _workspace(nb, workspace, logits)
     _launch("vq_balance_loss", dev, logits.data_ptr(), ids.data_ptr(), mp, T, E, ids.shape[1], coef, loss.data_ptr(),
             counts.data_ptr(), probs.data_ptr(), wp, nb)
     return loss, counts, probs

@@ -20,23 +20,27 @@ namespace {
 
 constexpr int BAL_WARPS = 16;            // warps per CTA
 constexpr int BAL_WIDE_WARPS = 8;        // the same for rows beyond BAL_REG_E: one row of sums per warp fits shared memory
+constexpr int BWD_WARPS = 8;             // warps per CTA of the gradient
 constexpr int BAL_ONE_CTA = 64;          // most tokens of the one-CTA form
-constexpr int BAL_PARTS = 148;           // most partial rows
+constexpr int BAL_PARTS = 296;           // most partial rows: 2 CTAs on each of 148 SMs (at most FIN_THREADS)
 constexpr int BAL_CLUSTER = 8;           // CTAs that add the partial rows
 constexpr int BAL_REG_E = 1024;          // widest row held in registers
 
+// Largest of the warp's values (one instruction on sm_100a; NaN is passed over).
 __device__ __forceinline__ float warp_max(float v)
 {
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(v));
+    return m;
 }
 
-// exp(l - top); a row of -Inf (top = -Inf) is taken as 0. NaN stays NaN.
-__device__ __forceinline__ float soft(float l, float top)
+// exp(l - top) as 2^((l - top) log2e). A row of -Inf (top = -Inf) is taken off 0 and gives 0; NaN stays NaN.
+__device__ __forceinline__ float base_of(float top) { return top == -INFINITY ? 0.f : top; }
+__device__ __forceinline__ float soft(float l, float base)
 {
-    return top == -INFINITY ? (l != l ? l : 0.f) : expf(l - top);
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((l - base) * 1.4426950408889634f));
+    return e;
 }
 
 // The expert in register i of a lane: VEC consecutive experts per lane and 32-lane sweep.
@@ -69,33 +73,82 @@ __device__ __forceinline__ float soften(float (&v)[PER])
 #pragma unroll
     for (int i = 0; i < PER; ++i)
         top = fmaxf(top, v[i]);
-    top = warp_max(top);
+    const float base = base_of(warp_max(top));
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        v[i] = soft(v[i], top);
+        v[i] = soft(v[i], base);
         s += v[i];
     }
     s = warp_total(s);
     return s == 0.f ? 0.f : 1.f / s;
 }
 
-// Column sums of warp-held rows: tokens t0 + warp, + warps, ...; acc[i] is expert_at(i)'s.
+// The first token at or after t, in steps of `step`, that counts.
+__device__ __forceinline__ long next_live(const uint8_t *mask, long t, long end, int step)
+{
+    while (mask && t < end && !mask[t])
+        t += step;
+    return t;
+}
+
+// Rows wider than 512 experts leave no registers for a row loaded ahead.
+template <int PER>
+constexpr bool AHEAD = PER <= 16;
+
+// The expert of lane j's pair of token t (j < k), -1 for none.
+__device__ __forceinline__ int pair_of(const BalanceArgs &a, long t, int lane)
+{
+    return lane < a.k ? a.ids[t * a.k + lane] : -1;
+}
+
+// Counts a token's pairs, and the token, into cnt[0..E] (shared). Integer sums: their order does not matter.
+__device__ __forceinline__ void count_token(int *cnt, int E, int e, int lane)
+{
+    if ((unsigned)e < (unsigned)E)
+        atomicAdd(&cnt[e], 1);
+    if (lane == 0)
+        atomicAdd(&cnt[E], 1);
+}
+
+// Column sums of warp-held rows: tokens t0 + warp, + NW, ...; acc[i] is
+// expert_at(i)'s; the tokens' pairs are counted on the way. The next row's
+// loads are under way while one is summed.
 template <int PER, int VEC, int NW>
-__device__ __forceinline__ void sum_rows(const BalanceArgs &a, long t0, long t1, int warp, int lane, float (&acc)[PER])
+__device__ __forceinline__ void sum_rows(const BalanceArgs &a, long t0, long t1, int warp, int lane, int *cnt,
+                                         float (&acc)[PER])
 {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
         acc[i] = 0.f;
-    for (long t = t0 + warp; t < t1; t += NW) {
-        if (a.mask && !a.mask[t])
-            continue;
-        float v[PER];
+    float v[PER], next[AHEAD<PER> ? PER : 1];
+    int e = -1, e_next = -1;
+    long t = next_live(a.mask, t0 + warp, t1, NW);
+    if (t < t1) {
         load_row<PER, VEC>(a.logits + t * a.E, a.E, lane, v);
+        e = pair_of(a, t, lane);
+    }
+    while (t < t1) {
+        const long u = next_live(a.mask, t + NW, t1, NW);
+        if (u < t1) {
+            if constexpr (AHEAD<PER>)
+                load_row<PER, VEC>(a.logits + u * a.E, a.E, lane, next);
+            e_next = pair_of(a, u, lane);
+        }
         const float inv = soften(v);
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             acc[i] = fmaf(v[i], inv, acc[i]);
+        count_token(cnt, a.E, e, lane);
+        if constexpr (AHEAD<PER>) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                v[i] = next[i];
+        } else if (u < t1) {
+            load_row<PER, VEC>(a.logits + u * a.E, a.E, lane, v);
+        }
+        e = e_next;
+        t = u;
     }
 }
 
@@ -108,29 +161,9 @@ __device__ __forceinline__ float excess(int count, int E, int V, int k, float pp
     return (float)((long)count * E - (long)V * k) * pp;
 }
 
-// Counts a CTA's pairs and valid tokens into cnt[0..E] (shared, zeroed here).
-__device__ __forceinline__ void count_pairs(const BalanceArgs &a, long t0, long t1, int *cnt)
-{
-    for (int e = threadIdx.x; e <= a.E; e += blockDim.x)
-        cnt[e] = 0;
-    __syncthreads();
-    const int k = a.k;
-    for (long p = t0 * k + threadIdx.x; p < t1 * k; p += blockDim.x) {
-        const long t = p / k;
-        if (a.mask && !a.mask[t])
-            continue;
-        const int e = a.ids[p];
-        if ((unsigned)e < (unsigned)a.E)
-            atomicAdd(&cnt[e], 1);
-        if (p == t * k)
-            atomicAdd(&cnt[a.E], 1);
-    }
-    __syncthreads();
-}
-
 // PER == 0: rows wider than BAL_REG_E, column sums in shared memory, one row of E per warp.
 template <int PER, int VEC>
-__global__ void __launch_bounds__((PER > 0 ? BAL_WARPS : BAL_WIDE_WARPS) * 32)
+__global__ void __launch_bounds__((PER > 0 ? BAL_WARPS : BAL_WIDE_WARPS) * 32, PER > 0 && AHEAD<PER> ? 2 : 1)
     vq_balance_kernel(const BalanceArgs a, int per_cta, int one)
 {
     constexpr int NW = PER > 0 ? BAL_WARPS : BAL_WIDE_WARPS, THREADS = NW * 32;
@@ -142,10 +175,12 @@ __global__ void __launch_bounds__((PER > 0 ? BAL_WARPS : BAL_WIDE_WARPS) * 32)
     grid_dep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.E;
     const long t0 = min((long)a.T, (long)blockIdx.x * per_cta), t1 = min((long)a.T, t0 + per_cta);
-    count_pairs(a, t0, t1, cnt);
+    for (int e = threadIdx.x; e <= E; e += THREADS)
+        cnt[e] = 0;
+    __syncthreads();
     if constexpr (PER > 0) {
         float acc[PER];
-        sum_rows<PER, VEC, NW>(a, t0, t1, warp, lane, acc);
+        sum_rows<PER, VEC, NW>(a, t0, t1, warp, lane, cnt, acc);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int e = expert_at<VEC>(i, lane);
@@ -158,17 +193,18 @@ __global__ void __launch_bounds__((PER > 0 ? BAL_WARPS : BAL_WIDE_WARPS) * 32)
         for (long t = t0 + warp; t < t1; t += NW) {
             if (a.mask && !a.mask[t])
                 continue;
+            count_token(cnt, E, pair_of(a, t, lane), lane);
             const float *l = a.logits + t * E;
             float top = -INFINITY, s = 0.f;
             for (int e = lane; e < E; e += 32)
                 top = fmaxf(top, l[e]);
-            top = warp_max(top);
+            const float base = base_of(warp_max(top));
             for (int e = lane; e < E; e += 32)
-                s += soft(l[e], top);
+                s += soft(l[e], base);
             s = warp_total(s);
             const float inv = s == 0.f ? 0.f : 1.f / s;
             for (int e = lane; e < E; e += 32)
-                sums[warp * E + e] = fmaf(soft(l[e], top), inv, sums[warp * E + e]);
+                sums[warp * E + e] = fmaf(soft(l[e], base), inv, sums[warp * E + e]);
         }
     }
     __syncthreads();
@@ -220,55 +256,49 @@ constexpr int FIN_THREADS = 1024;
 __global__ void __cluster_dims__(BAL_CLUSTER, 1, 1) __launch_bounds__(FIN_THREADS)
     vq_balance_finish_kernel(const BalanceArgs a, int parts)
 {
-    __shared__ float fs[FIN_THREADS];
-    __shared__ int is[FIN_THREADS];
-    __shared__ float term;
+    __shared__ float fs[FIN_THREADS], term, red[FIN_THREADS / 32];
+    __shared__ int is[FIN_THREADS], valid[FIN_THREADS / 32];
     grid_dep_launch();
     grid_dep_wait();
-    const int E = a.E, rank = blockIdx.x, tid = threadIdx.x;
-    // the tokens that count, by every CTA for itself
-    int v = 0;
-    for (int p = tid; p < parts; p += FIN_THREADS)
-        v += a.part_counts[(long)p * (E + 1) + E];
-    is[tid] = v;
-    __syncthreads();
-    for (int o = FIN_THREADS / 2; o; o >>= 1) {
-        if (tid < o)
-            is[tid] += is[tid + o];
-        __syncthreads();
-    }
-    const int V = is[0];
-    const float pp = per_pair(V, a.k);
-    __syncthreads();
-    const int per = (E + BAL_CLUSTER - 1) / BAL_CLUSTER, e0 = rank * per, e1 = min(E, e0 + per);
-    float loss = 0.f;
-    // 32 experts at a time, 32 strands of partial rows each
-    for (int b = e0; b < e1; b += 32) {
-        const int e = b + (tid & 31);
-        float s = 0.f;
-        int c = 0;
-        if (e < e1)
-            for (int p = tid >> 5; p < parts; p += 32) {
-                s += a.part_sums[(long)p * E + e];
-                c += a.part_counts[(long)p * (E + 1) + e];
-            }
-        fs[tid] = s;
-        is[tid] = c;
-        __syncthreads();
-        if (tid < 32 && e < e1) {
-            s = 0.f;
-            c = 0;
-            for (int i = 0; i < 32; ++i) {
-                s += fs[i * 32 + tid];
-                c += is[i * 32 + tid];
-            }
-            s = V ? s / (float)V : 0.f;
-            a.probs[e] = s;
-            a.counts[e] = c;
-            loss = fmaf(share(c, E, pp), s, loss);
+    const int E = a.E, rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+    // a thread: one expert of the CTA's slice (at most 512), one of `strands` interleaved strands of partial rows
+    const int per = (E + BAL_CLUSTER - 1) / BAL_CLUSTER, width = per <= 32 ? 32 : per <= 64 ? 64 : per <= 128 ? 128 : per <= 256 ? 256 : 512;
+    const int strands = FIN_THREADS / width, x = tid & (width - 1), e = rank * per + x;
+    const bool mine = x < per && e < E;
+    float s = 0.f;
+    int c = 0;
+    if (mine) {
+#pragma unroll 4
+        for (int p = tid / width; p < parts; p += strands) {
+            s += a.part_sums[(long)p * E + e];
+            c += a.part_counts[(long)p * (E + 1) + e];
         }
-        __syncthreads();
     }
+    fs[tid] = s;
+    is[tid] = c;
+    // the tokens that count, by every CTA for itself
+    const int v = __reduce_add_sync(0xFFFFFFFFu, tid < parts ? a.part_counts[(long)tid * (E + 1) + E] : 0);
+    if (lane == 0)
+        valid[tid >> 5] = v;
+    __syncthreads();
+    const int V = __reduce_add_sync(0xFFFFFFFFu, valid[lane]);
+    const float pp = per_pair(V, a.k);
+    float loss = 0.f;
+    if (tid < width && mine) {
+        for (int i = 1; i < strands; ++i) {
+            s += fs[i * width + tid];
+            c += is[i * width + tid];
+        }
+        s = V ? s / (float)V : 0.f;
+        a.probs[e] = s;
+        a.counts[e] = c;
+        loss = share(c, E, pp) * s;
+    }
+    loss = warp_total(loss);
+    if (lane == 0)
+        red[tid >> 5] = loss;
+    __syncthreads();
+    loss = red[lane];
     if (tid < 32) {
         loss = warp_total(loss);
         if (tid == 0)
@@ -308,7 +338,7 @@ __global__ void vq_balance_empty_kernel(const BalanceArgs a)
 // ---------------------------------------------------------------- gradient
 
 template <int PER, int VEC>
-__global__ void __launch_bounds__(BAL_WARPS * 32) vq_balance_bwd_kernel(const BalanceBwdArgs a)
+__global__ void __launch_bounds__(BWD_WARPS * 32) vq_balance_bwd_kernel(const BalanceBwdArgs a)
 {
     grid_dep_launch();
     grid_dep_wait();
@@ -316,25 +346,42 @@ __global__ void __launch_bounds__(BAL_WARPS * 32) vq_balance_bwd_kernel(const Ba
     const int V = a.counts[E];
     const float scale = V ? (a.dloss ? *a.dloss : 1.f) * a.coef / (float)V : 0.f;
     const float pp = per_pair(V, a.k);
-    const int step = gridDim.x * BAL_WARPS;
+    const int step = gridDim.x * BWD_WARPS;
     constexpr int N = PER > 0 ? PER : 1;
-    float d[N];
+    float d[N], next[PER > 0 && AHEAD<PER> ? PER : 1];
+    auto counts = [&](long t) { return V && (!a.mask || a.mask[t]); };
+    long t = (long)blockIdx.x * BWD_WARPS + warp;
+    bool live = t < a.T && counts(t);
     if constexpr (PER > 0) {
+        if constexpr (AHEAD<PER>)
+            if (live)
+                load_row<PER, VEC>(a.logits + t * E, E, lane, next);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int e = expert_at<VEC>(i, lane);
             d[i] = e < E ? excess(a.counts[e], E, V, a.k, pp) : 0.f;
         }
     }
-    for (long t = (long)blockIdx.x * BAL_WARPS + warp; t < a.T; t += step) {
+    for (; t < a.T; t += step) {
         const float *l = a.logits + t * E;
         float *o = a.dlogits + t * E;
-        const bool live = V && (!a.mask || a.mask[t]);
         if constexpr (PER > 0) {
             float v[PER];
+            const bool now = live;
+            if constexpr (AHEAD<PER>) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    v[i] = next[i];
+                live = t + step < a.T && counts(t + step);
+                if (live)
+                    load_row<PER, VEC>(l + (long)step * E, E, lane, next);
+            } else {
+                if (now)
+                    load_row<PER, VEC>(l, E, lane, v);
+                live = t + step < a.T && counts(t + step);
+            }
             float dot = 0.f, inv = 0.f;
-            if (live) {
-                load_row<PER, VEC>(l, E, lane, v);
+            if (now) {
                 inv = soften(v);
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
@@ -344,7 +391,7 @@ __global__ void __launch_bounds__(BAL_WARPS * 32) vq_balance_bwd_kernel(const Ba
             }
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                v[i] = live ? v[i] * inv * (d[i] - dot) : 0.f;
+                v[i] = now ? v[i] * inv * (d[i] - dot) : 0.f;
 #pragma unroll
             for (int i = 0; i < PER; i += VEC) {
                 const int e = expert_at<VEC>(i, lane);
@@ -356,7 +403,7 @@ __global__ void __launch_bounds__(BAL_WARPS * 32) vq_balance_bwd_kernel(const Ba
                 }
             }
         } else {
-            if (!live) {
+            if (!counts(t)) {
                 for (int e = lane; e < E; e += 32)
                     o[e] = 0.f;
                 continue;
@@ -364,9 +411,9 @@ __global__ void __launch_bounds__(BAL_WARPS * 32) vq_balance_bwd_kernel(const Ba
             float top = -INFINITY, s = 0.f, dot = 0.f;
             for (int e = lane; e < E; e += 32)
                 top = fmaxf(top, l[e]);
-            top = warp_max(top);
+            const float base = base_of(warp_max(top));
             for (int e = lane; e < E; e += 32) {
-                const float p = soft(l[e], top);
+                const float p = soft(l[e], base);
                 s += p;
                 dot = fmaf(p, excess(a.counts[e], E, V, a.k, pp), dot);
             }
@@ -374,7 +421,7 @@ __global__ void __launch_bounds__(BAL_WARPS * 32) vq_balance_bwd_kernel(const Ba
             const float inv = s == 0.f ? 0.f : 1.f / s;
             dot = warp_total(dot) * inv;
             for (int e = lane; e < E; e += 32)
-                o[e] = soft(l[e], top) * (inv * scale) * (excess(a.counts[e], E, V, a.k, pp) - dot);
+                o[e] = soft(l[e], base) * (inv * scale) * (excess(a.counts[e], E, V, a.k, pp) - dot);
         }
     }
 }
@@ -398,14 +445,17 @@ cudaError_t fwd(const BalanceArgs &a, int ctas, int per_cta, int one, cudaStream
 template <int PER, int VEC>
 cudaError_t bwd(const BalanceBwdArgs &a, cudaStream_t s)
 {
-    const int ctas = (int)std::min(((long)a.T + BAL_WARPS - 1) / BAL_WARPS, 8L * 148);
-    return launch_after(vq_balance_bwd_kernel<PER, VEC>, dim3(ctas), dim3(BAL_WARPS * 32), 0, s, a);
+    // persistent warps: 3 CTAs of 8 on an SM
+    const int ctas = (int)std::min(((long)a.T + BWD_WARPS - 1) / BWD_WARPS, 3L * 148);
+    return launch_after(vq_balance_bwd_kernel<PER, VEC>, dim3(ctas), dim3(BWD_WARPS * 32), 0, s, a);
 }
 
 }  // namespace
 
 size_t balance_workspace_bytes(int T, int E)
 {
+    if (T <= BAL_ONE_CTA)
+        return 0;
     return align_up((size_t)BAL_PARTS * E * 4, 256) + align_up((size_t)BAL_PARTS * (E + 1) * 4, 256);
 }
 
@@ -414,9 +464,11 @@ cudaError_t launch_balance(const BalanceArgs &args, void *ws, cudaStream_t s)
     BalanceArgs a = args;
     if (a.T == 0)
         return launch_after(vq_balance_empty_kernel, dim3(1), dim3(256), 0, s, a);
-    a.part_sums = static_cast<float *>(ws);
-    a.part_counts = ws_at<int32_t>(ws, align_up((size_t)BAL_PARTS * a.E * 4, 256));
     const int one = a.T <= BAL_ONE_CTA;
+    if (!one) {
+        a.part_sums = static_cast<float *>(ws);
+        a.part_counts = ws_at<int32_t>(ws, align_up((size_t)BAL_PARTS * a.E * 4, 256));
+    }
     const int per_cta = one ? a.T : std::max(BAL_WARPS, (int)(((long)a.T + BAL_PARTS - 1) / BAL_PARTS));
     const int ctas = (int)(((long)a.T + per_cta - 1) / per_cta);
     const bool v4 = a.E % 4 == 0 && (uintptr_t)a.logits % 16 == 0;

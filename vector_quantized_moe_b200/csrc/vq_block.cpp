@@ -318,7 +318,8 @@ vq_status vq_balance_loss(const float *logits, const int32_t *ids, const uint8_t
         return VQ_ERR_ARG;
     if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(probs, 4))
         return VQ_ERR_ALIGN;
-    const vq_status st = check_ws(workspace, ws_bytes, balance_workspace_bytes(T, E));
+    const size_t need = balance_workspace_bytes(T, E);
+    const vq_status st = need ? check_ws(workspace, ws_bytes, need) : VQ_OK;
     if (st != VQ_OK)
         return st;
     BalanceArgs a{};
