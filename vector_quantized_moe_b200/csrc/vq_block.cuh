@@ -288,12 +288,6 @@ __device__ __forceinline__ void ring_get(uint32_t at, uint32_t step, float2 (&v)
     c.get(v);
 }
 
-__device__ __forceinline__ void ring_put(uint32_t at, uint32_t step, const float2 (&v)[4])
-{
-    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y) : "memory");
-    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + step), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y) : "memory");
-}
-
 // The same for an array whose type is known at run time.
 __device__ __forceinline__ void ring_copy_any(uint32_t at, uint32_t step, const void *p, int dtype, long i)
 {
@@ -338,8 +332,8 @@ __device__ __forceinline__ float warp_total_from(float v)
     return v;
 }
 
-// Sums of N <= 3 values over the W warps of a row (one row per CTA when
-// W > 1), in a fixed order. Several values share the warp's shuffles: 5, 5 and
+// Sums of N <= 3 values over the W warps of a row, in a fixed order; rows side
+// by side in a CTA meet at barriers of their own. Several values share the warp's shuffles: 5, 5 and
 // 6 for 1, 2 and 3 values. Two buffers in turn: a warp may start the next sum
 // while another still reads this one.
 template <int N>
@@ -347,11 +341,18 @@ struct RowSum {
     float buf[2][N][32];
 };
 
+// A thread's place among the W warps of its row, R rows side by side in the CTA.
+struct RowTeam {
+    int W, R, tid, rg, warp;   // tid: thread of the row; rg: row of the CTA; warp: warp of the row
+    __device__ __forceinline__ explicit RowTeam(int w)
+        : W(w), R(blockDim.x / (32 * w)), tid(threadIdx.x % (32 * w)), rg(threadIdx.x / (32 * w)), warp(tid >> 5) {}
+};
+
 template <int N, int M>
-__device__ __forceinline__ void row_sum(float (&v)[N], RowSum<M> &s, int W, int &turn)
+__device__ __forceinline__ void row_sum(float (&v)[N], RowSum<M> &s, const RowTeam &m, int &turn)
 {
     static_assert(N <= M && N <= 3, "sums");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, W = m.W, first = m.rg * W;
     float x;        // lanes 0, 16, 8: totals of v[0], v[1], v[2]
     if constexpr (N == 1)
         x = warp_total_from<16>(v[0]);
@@ -368,27 +369,30 @@ __device__ __forceinline__ void row_sum(float (&v)[N], RowSum<M> &s, int W, int 
         return;
     }
     if (lane == 0)
-        s.buf[turn][0][warp] = x;
+        s.buf[turn][0][first + m.warp] = x;
     if (N > 1 && lane == 16)
-        s.buf[turn][N > 1 ? 1 : 0][warp] = x;
+        s.buf[turn][N > 1 ? 1 : 0][first + m.warp] = x;
     if (N > 2 && lane == 8)
-        s.buf[turn][N > 2 ? 2 : 0][warp] = x;
-    __syncthreads();
+        s.buf[turn][N > 2 ? 2 : 0][first + m.warp] = x;
+    if (m.R == 1)
+        __syncthreads();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + m.rg), "r"(32 * W) : "memory");
     if (W <= 16) {
         const int l = lane & 15;
         if constexpr (N == 1) {
-            v[0] = warp_total_from<8>(l < W ? s.buf[turn][0][l] : 0.f);
+            v[0] = warp_total_from<8>(l < W ? s.buf[turn][0][first + l] : 0.f);
         } else {
-            x = warp_total_from<8>(l < W ? s.buf[turn][lane >> 4][l] : 0.f);
+            x = warp_total_from<8>(l < W ? s.buf[turn][lane >> 4][first + l] : 0.f);
             v[0] = __shfl_sync(0xFFFFFFFFu, x, 0);
             v[1] = __shfl_sync(0xFFFFFFFFu, x, 16);
             if constexpr (N > 2)
-                v[2] = warp_total_from<8>(l < W ? s.buf[turn][2][l] : 0.f);
+                v[2] = warp_total_from<8>(l < W ? s.buf[turn][2][first + l] : 0.f);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            v[i] = warp_total_from<16>(lane < W ? s.buf[turn][i][lane] : 0.f);
+            v[i] = warp_total_from<16>(lane < W ? s.buf[turn][i][first + lane] : 0.f);
     }
     turn ^= 1;
 }

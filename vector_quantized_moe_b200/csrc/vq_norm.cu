@@ -30,8 +30,9 @@ __global__ void __launch_bounds__(1024) vq_norm_pre_scalar_kernel(const NormPreA
     __shared__ RowSum<1> rs;
     grid_dep_launch();
     grid_dep_wait();
-    const int W = a.W, tid = threadIdx.x % (32 * W);
-    const long row = (long)blockIdx.x * (blockDim.x / (32 * W)) + threadIdx.x / (32 * W);
+    const RowTeam team(a.W);
+    const int W = team.W, tid = team.tid;
+    const long row = (long)blockIdx.x * team.R + team.rg;
     if (row >= a.T)   // only in CTAs of one-warp rows, which never meet at a barrier
         return;
     const HT *h = static_cast<const HT *>(a.h) + row * a.h_ld;
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(1024) vq_norm_pre_scalar_kernel(const NormPreA
         }
     }
     int turn = 0;
-    row_sum(ss, rs, W, turn);
+    row_sum(ss, rs, team, turn);
     const float r = rsqrtf(ss[0] * a.inv_h + a.n.eps);
     uint16_t *x = a.x + row * a.x_ld;
 #pragma unroll
@@ -88,8 +89,9 @@ __global__ void __launch_bounds__(1024) vq_norm_post_scalar_kernel(const NormPos
     __shared__ RowSum<1> rs;
     grid_dep_launch();
     grid_dep_wait();
-    const int W = a.W, tid = threadIdx.x % (32 * W);
-    const long row = (long)blockIdx.x * (blockDim.x / (32 * W)) + threadIdx.x / (32 * W);
+    const RowTeam team(a.W);
+    const int W = team.W, tid = team.tid;
+    const long row = (long)blockIdx.x * team.R + team.rg;
     if (row >= a.T)
         return;
     const YT *y = static_cast<const YT *>(a.y) + row * a.y_ld;
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(1024) vq_norm_post_scalar_kernel(const NormPos
                 for (int j = 0; j < VEC; ++j)
                     ss[0] = fmaf(v[j], v[j], ss[0]);
             }
-        row_sum(ss, rs, W, turn);
+        row_sum(ss, rs, team, turn);
         r1 = rsqrtf(ss[0] * a.inv_h + a.post.eps);
     }
     float ss[1] = {0.f};
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(1024) vq_norm_post_scalar_kernel(const NormPos
     }
     if (!a.next.weight)
         return;
-    row_sum(ss, rs, W, turn);
+    row_sum(ss, rs, team, turn);
     const float r2 = rsqrtf(ss[0] * a.inv_h + a.next.eps);
     uint16_t *x = a.x + row * a.x_ld;
 #pragma unroll
@@ -211,8 +213,9 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_kernel(const NormPreA
     __shared__ RowSum<1> rs;
     extern __shared__ __align__(16) unsigned char ring[];
     constexpr int PH = PIECES<HT>, P = NV * PH;
-    const int W = a.W, tid = threadIdx.x % (32 * W), R = blockDim.x / (32 * W), stride = gridDim.x * R;
-    const long row0 = (long)blockIdx.x * R + threadIdx.x / (32 * W);
+    const RowTeam team(a.W);
+    const int W = team.W, tid = team.tid, R = team.R, stride = gridDim.x * R;
+    const long row0 = (long)blockIdx.x * R + team.rg;
     const uint32_t step = blockDim.x * 16, base = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
     const int hop = 256 * W;   // elements from a thread's chunk to its next
     const HT *h = static_cast<const HT *>(a.h) + row0 * a.h_ld + tid * 8;
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_kernel(const NormPreA
                     sq = fma2(v[i][j], v[i][j], sq);
             }
         float ss[1] = {sq.x + sq.y};
-        row_sum(ss, rs, W, turn);
+        row_sum(ss, rs, team, turn);
         const float r = rsqrtf(ss[0] * a.inv_h + a.n.eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -288,8 +291,9 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_kernel(const NormPos
     constexpr int PY = PIECES<YT>, PH = PIECES<HT>, OH = NV * PY, OZ = OH + NV * PH;
     const bool post = a.post.weight != nullptr, next = a.next.weight != nullptr;
     const int pz = a.gate_mode != GATE_CHANNEL ? 0 : a.gate_dtype == VQ_F32 ? 2 : 1, P = OZ + NV * pz;
-    const int W = a.W, tid = threadIdx.x % (32 * W), R = blockDim.x / (32 * W), stride = gridDim.x * R;
-    const long row0 = (long)blockIdx.x * R + threadIdx.x / (32 * W);
+    const RowTeam team(a.W);
+    const int W = team.W, tid = team.tid, R = team.R, stride = gridDim.x * R;
+    const long row0 = (long)blockIdx.x * R + team.rg;
     const uint32_t step = blockDim.x * 16, base = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
     const int hop = 256 * W;   // elements from a thread's chunk to its next
     const YT *y = static_cast<const YT *>(a.y) + row0 * a.y_ld + tid * 8;
@@ -366,7 +370,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_kernel(const NormPos
             }
         if (post) {
             float ss[1] = {sq.x + sq.y};
-            row_sum(ss, rs, W, turn);
+            row_sum(ss, rs, team, turn);
             f *= rsqrtf(ss[0] * a.inv_h + a.post.eps);
         }
         sq = splat(0.f);
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_kernel(const NormPos
         ho += stride * a.ho_ld;
         if (next) {
             float ss[1] = {sq.x + sq.y};
-            row_sum(ss, rs, W, turn);
+            row_sum(ss, rs, team, turn);
             const float r2 = rsqrtf(ss[0] * a.inv_h + a.next.eps);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -491,17 +495,22 @@ NormShape norm_shape(int H, int T, int bytes, int fixed, const int (&regs)[4], i
     s.nv = (chunks + threads - 1) / threads;
     s.W = ((chunks + s.nv - 1) / s.nv + 31) / 32;
     s.R = s.W == 1 ? 8 : 1;
+    const size_t row = (size_t)32 * s.W * 8 * s.nv, keep = row * fixed, room = NORM_SMEM;
+    // with weights in shared memory: rows side by side share them, up to ROW_THREADS threads
+    if (fixed && T > 2 * 148)
+        while (2 * s.R * 32 * s.W <= ROW_THREADS && 2 * 2 * s.R * row * bytes + keep <= room)
+            s.R *= 2;
     const int block = 32 * s.W * s.R;
-    const size_t row = (size_t)block * 8 * s.nv, stage = row * bytes, keep = row * fixed, room = NORM_SMEM;
+    const size_t stage = row * s.R * bytes;
     s.S = s.ctas = 0;
     s.smem = 0;
     if (stage + keep > room)
         return s;
     // two rows ahead where they fit, then as many CTAs as registers and shared memory allow
     int per_sm = std::max(1, std::min(16, 65536 / (regs[s.nv - 1] * block)));
-    while (per_sm > 1 && per_sm * (2 * stage + keep) > room)
+    while (per_sm > 1 && per_sm * (2 * stage + keep + 2048) > room)
         --per_sm;
-    s.S = (int)std::min<size_t>(4, (room / per_sm - keep) / stage);
+    s.S = (int)std::min<size_t>(4, (room / per_sm - keep - (per_sm > 1 ? 2048 : 0)) / stage);
     long ctas = std::min(((long)T + s.R - 1) / s.R, 148L * per_sm);
     if (max_ctas)
         ctas = std::min<long>(ctas, max_ctas);

@@ -27,8 +27,9 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_bwd_scalar_kernel(con
     __shared__ RowSum<2> rs;
     grid_dep_launch();
     grid_dep_wait();
-    const int W = a.W, tid = threadIdx.x % (32 * W), R = blockDim.x / (32 * W);
-    const int slot = blockIdx.x * R + threadIdx.x / (32 * W);
+    const RowTeam team(a.W);
+    const int W = team.W, tid = team.tid, R = team.R;
+    const int slot = blockIdx.x * R + team.rg;
     float acc[NV][VEC];
     AnyChunk<VEC> wc[NV];
 #pragma unroll
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_bwd_scalar_kernel(con
                     s[1] = fmaf(d[j] * (w[j] + a.n.offset), v[j], s[1]);
                 }
             }
-        row_sum(s, rs, W, turn);
+        row_sum(s, rs, team, turn);
         const float r = rsqrtf(s[0] * a.inv_h + a.n.eps);
         const float m = r * (s[1] * a.inv_h);   // mean(g v^)
 #pragma unroll
@@ -118,8 +119,9 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_scalar_kernel(co
     __shared__ RowSum<3> rs;
     grid_dep_launch();
     grid_dep_wait();
-    const int W = a.W, tid = threadIdx.x % (32 * W), R = blockDim.x / (32 * W);
-    const int slot = blockIdx.x * R + threadIdx.x / (32 * W);
+    const RowTeam team(a.W);
+    const int W = team.W, tid = team.tid, R = team.R;
+    const int slot = blockIdx.x * R + team.rg;
     const bool post = a.post.weight != nullptr, next = a.next.weight != nullptr;
     float acc1[NV][VEC], acc2[NV][VEC];
     AnyChunk<VEC> w1[NV], w2[NV];
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_scalar_kernel(co
                 }
             }
         if (next || post)
-            row_sum(s, rs, W, turn);
+            row_sum(s, rs, team, turn);
         const float r2 = rsqrtf(s[0] * a.inv_h + a.next.eps), m2 = r2 * (s[1] * a.inv_h);
         const float r1 = post ? rsqrtf(s[2] * a.inv_h + a.post.eps) : 1.f;
         float dH[NV][VEC];
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_scalar_kernel(co
             }
         }
         if (post || (a.gate_mode == GATE_TOKEN && a.dgate))
-            row_sum(q, rs, W, turn);
+            row_sum(q, rs, team, turn);
         if (a.gate_mode == GATE_TOKEN && a.dgate && tid == 0) {
             const float dz = q[1] * on * off;
             const long at = row * a.dgate_ld;
@@ -309,47 +311,59 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_scalar_kernel(co
 
 // ---------------------------------------------------------------- rows on 16-byte boundaries, copied ahead
 
-// A CTA's weight gradient: its side-by-side rows' sums added in order into one partial row.
+// A CTA's weight gradient: the sums of its side-by-side rows added in order
+// into one partial row. side: H floats of shared memory.
 template <int NV>
-__device__ __forceinline__ void write_part(float *part, const float2 (&acc)[NV][4], float *side, int tid, int W, int H)
+__device__ __forceinline__ void write_part(float *part, float2 (&acc)[NV][4], float *side, int tid, int W, int H)
 {
     const int R = blockDim.x / (32 * W), rg = threadIdx.x / (32 * W);
-    if (R > 1) {   // one-warp rows (NV = 1): side is [R][256]
+    for (int r = 1; r < R; ++r) {
         __syncthreads();
+        if (rg == r)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<float2 *>(&side[rg * 256 + tid * 8 + 2 * j]) = acc[0][j];
+            for (int i = 0; i < NV; ++i)
+                if (chunk_at<8>(i, tid, W) < H) {
+                    Chunk<float, 8> o;
+                    o.set(acc[i]);
+                    o.store(side + chunk_at<8>(i, tid, W));
+                }
         __syncthreads();
-        for (int c = threadIdx.x; c < H; c += blockDim.x) {
-            float v = side[c];
-            for (int r = 1; r < R; ++r)
-                v += side[r * 256 + c];
-            part[(long)blockIdx.x * H + c] = v;
-        }
-        return;
-    }
+        if (rg == 0)
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = chunk_at<8>(i, tid, W);
-        if (c < H) {
-            Chunk<float, 8> o;
-            o.set(acc[i]);
-            o.store(part + (long)blockIdx.x * H + c);
-        }
+            for (int i = 0; i < NV; ++i)
+                if (chunk_at<8>(i, tid, W) < H) {
+                    Chunk<float, 8> o;
+                    float2 v[4];
+                    o.load(side + chunk_at<8>(i, tid, W));
+                    o.get(v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[i][j] = add2(acc[i][j], v[j]);
+                }
     }
+    if (rg == 0)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = chunk_at<8>(i, tid, W);
+            if (c < H) {
+                Chunk<float, 8> o;
+                o.set(acc[i]);
+                o.store(part + (long)blockIdx.x * H + c);
+            }
+        }
 }
 
 template <typename HT, int NV>
 __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_bwd_kernel(const NormPreBwdArgs a, int S)
 {
     __shared__ RowSum<2> rs;
-    __shared__ float side[NV == 1 ? 8 * 256 : 1];
     extern __shared__ __align__(16) unsigned char ring[];
     constexpr int PH = PIECES<HT>, OX = NV * PH, OR = OX + NV;   // pieces: h, dx, dres
     const bool res = a.dres != nullptr;
     const int P = OR + (res ? NV * PH : 0);
-    const int W = a.W, tid = threadIdx.x % (32 * W), R = blockDim.x / (32 * W), stride = gridDim.x * R;
-    const long row0 = (long)blockIdx.x * R + threadIdx.x / (32 * W);
+    const RowTeam team(a.W);
+    const int W = team.W, tid = team.tid, R = team.R, stride = gridDim.x * R;
+    const long row0 = (long)blockIdx.x * R + team.rg;
     const uint32_t step = blockDim.x * 16, base = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
     const int hop = 256 * W;   // elements from a thread's chunk to its next
     const HT *h = static_cast<const HT *>(a.h) + row0 * a.h_ld + tid * 8;
@@ -417,7 +431,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_bwd_kernel(const Norm
                 }
             }
         float q[2] = {q0.x + q0.y, q1.x + q1.y};
-        row_sum(q, rs, W, turn);
+        row_sum(q, rs, team, turn);
         const float r = rsqrtf(q[0] * a.inv_h + a.n.eps);
         const float rm = r * (r * (q[1] * a.inv_h));   // r mean(g v^)
 #pragma unroll
@@ -444,26 +458,30 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_bwd_kernel(const Norm
         dh += stride * a.dh_ld;
     }
     if (a.part)
-        write_part(a.part, acc, side, tid, W, a.H);
+        write_part(a.part, acc, reinterpret_cast<float *>(ring), tid, W, a.H);
 }
 
-// The weights (offset added, fp32) of a thread's columns sit in shared memory
-// behind the ring: with two weight gradients a thread has no registers for them.
+// The weights of a thread's columns sit in shared memory behind the ring: with
+// two weight gradients a thread has no registers for them.
 template <typename YT, typename HT, int NV>
 __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const NormPostBwdArgs a, int S)
 {
     __shared__ RowSum<3> rs;
-    __shared__ float side[NV == 1 ? 8 * 256 : 1];
     extern __shared__ __align__(16) unsigned char ring[];
     const bool post = a.post.weight != nullptr, next = a.next.weight != nullptr, has = a.dho != nullptr;
     // pieces of a stage: y, dh_out, h_out and dx_out (with the next norm), per-channel gates
     constexpr int PY = PIECES<YT>, PH = PIECES<HT>, OG = NV * PY;
     const int OH = OG + (has ? NV * PH : 0), OX = OH + (next ? NV * PH : 0), OZ = OX + (next ? NV : 0);
     const int pz = a.gate_mode != GATE_CHANNEL ? 0 : a.gate_dtype == VQ_F32 ? 2 : 1, P = OZ + NV * pz;
-    const int W = a.W, tid = threadIdx.x % (32 * W), R = blockDim.x / (32 * W), stride = gridDim.x * R;
-    const long row0 = (long)blockIdx.x * R + threadIdx.x / (32 * W);
+    const RowTeam team(a.W);
+    const int W = team.W, tid = team.tid, R = team.R, stride = gridDim.x * R;
+    const long row0 = (long)blockIdx.x * R + team.rg;
     const uint32_t step = blockDim.x * 16, base = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
-    const uint32_t at1 = base + S * P * step, at2 = at1 + (post ? 2 * NV * step : 0);   // the weights
+    // the weights, one copy for all rows side by side
+    const uint32_t wstep = 32 * W * 16;
+    const uint32_t at1 = (uint32_t)__cvta_generic_to_shared(ring) + S * P * step + tid * 16;
+    const int p1 = !post ? 0 : a.post.dtype == VQ_F32 ? 2 : 1, p2 = a.next.dtype == VQ_F32 ? 2 : 1;
+    const uint32_t at2 = at1 + p1 * NV * wstep;
     const int hop = 256 * W;   // elements from a thread's chunk to its next
     const YT *y = static_cast<const YT *>(a.y) + row0 * a.y_ld + tid * 8;
     const HT *h = static_cast<const HT *>(a.h) + row0 * a.h_ld + tid * 8;
@@ -503,24 +521,25 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
     };
     grid_dep_launch();
     grid_dep_wait();
-    for (int s = 0; s < S - 1; ++s)
-        fetch(s);
     float2 acc1[NV][4], acc2[NV][4];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float2 w[4];
-        if (in[i] && post) {
-            load_weight(a.post.weight, a.post.dtype, a.post.offset, chunk_at<8>(i, tid, W), w);
-            ring_put(at1 + 2 * i * step, step, w);
-        }
-        if (in[i] && next) {
-            load_weight(a.next.weight, a.next.dtype, a.next.offset, chunk_at<8>(i, tid, W), w);
-            ring_put(at2 + 2 * i * step, step, w);
-        }
+    for (int i = 0; i < NV; ++i) {   // the weights come with the first row's copies
+        if (in[i] && post)
+            ring_copy_any(at1 + p1 * i * wstep, wstep, a.post.weight, a.post.dtype, chunk_at<8>(i, tid, W));
+        if (in[i] && next)
+            ring_copy_any(at2 + p2 * i * wstep, wstep, a.next.weight, a.next.dtype, chunk_at<8>(i, tid, W));
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             acc1[i][j] = acc2[i][j] = splat(0.f);
     }
+    for (int s = 0; s < S - 1; ++s)
+        fetch(s);
+    auto weight = [&](uint32_t at, const NormDev &n, float2 (&w)[4]) {
+        ring_get_any(at, wstep, n.dtype, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = add2(w[j], splat(n.offset));
+    };
     int turn = 0, s = 0;
     for (long row = row0; row < a.T; row += stride) {
         float on = 1.f, off = 0.f;   // sigmoid(z), 1 - sigmoid(z)
@@ -549,7 +568,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
                 if (next) {
                     ring_get<HT>(at + (OH + i * PH) * step, step, v);
                     ring_get<uint16_t>(at + (OX + i) * step, step, d);
-                    ring_get<float>(at2 + 2 * i * step, step, w);
+                    weight(at2 + p2 * i * wstep, a.next, w);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         q0 = fma2(v[j], v[j], q0);
@@ -565,7 +584,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
             }
         float q[3] = {q0.x + q0.y, q1.x + q1.y, q2.x + q2.y};
         if (next || post)
-            row_sum(q, rs, W, turn);
+            row_sum(q, rs, team, turn);
         const float r2 = rsqrtf(q[0] * a.inv_h + a.next.eps), rm2 = r2 * (r2 * (q[1] * a.inv_h));
         const float r1 = post ? rsqrtf(q[2] * a.inv_h + a.post.eps) : 1.f;
         float2 dH[NV][4], t0 = splat(0.f);   // t0: sum g y of the post norm (channel gates), or sum dv u
@@ -582,7 +601,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
                     float2 d[4];
                     ring_get<HT>(at + (OH + i * PH) * step, step, v);
                     ring_get<uint16_t>(at + (OX + i) * step, step, d);
-                    ring_get<float>(at2 + 2 * i * step, step, w);
+                    weight(at2 + p2 * i * wstep, a.next, w);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float2 n = mul2(v[j], splat(r2));
@@ -603,7 +622,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
                 for (int j = 0; j < 4; ++j)
                     w[j] = splat(1.f);
                 if (post)
-                    ring_get<float>(at1 + 2 * i * step, step, w);
+                    weight(at1 + p1 * i * wstep, a.post, w);
                 if (pz) {
                     float2 z[4];
                     ring_get_any(at + (OZ + i * pz) * step, step, a.gate_dtype, z);
@@ -645,7 +664,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
         const bool token = a.gate_mode == GATE_TOKEN && a.dgate;
         float t[1] = {t0.x + t0.y};
         if (post || token)
-            row_sum(t, rs, W, turn);
+            row_sum(t, rs, team, turn);
         if (token && tid == 0) {
             const float dz = t[0] * on * off;
             const long to = row * a.dgate_ld;
@@ -673,9 +692,9 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
         dy += stride * a.dy_ld;
     }
     if (a.part1)
-        write_part(a.part1, acc1, side, tid, W, a.H);
+        write_part(a.part1, acc1, reinterpret_cast<float *>(ring), tid, W, a.H);
     if (a.part2)
-        write_part(a.part2, acc2, side, tid, W, a.H);
+        write_part(a.part2, acc2, reinterpret_cast<float *>(ring), tid, W, a.H);
 }
 
 // Column sums of the partial rows, in row order within each of 8 interleaved
@@ -762,8 +781,9 @@ template <typename YT, typename HT>
 cudaError_t post_bwd(NormPostBwdArgs a, bool vec8, int &parts, cudaStream_t s)
 {
     const int gate = a.gate_mode != GATE_CHANNEL ? 0 : a.gate_dtype == VQ_F32 ? 4 : 2;
+    auto w = [](const NormDev &n) { return !n.weight ? 0 : n.dtype == VQ_F32 ? 4 : 2; };
     NormShape sh = norm_shape(a.H, a.T, sizeof(YT) + (a.dho ? sizeof(HT) : 0) + (a.next.weight ? sizeof(HT) + 2 : 0) + gate,
-                              (a.post.weight ? 4 : 0) + (a.next.weight ? 4 : 0), POST_BWD_REGS, 512, NORM_PARTS);
+                              w(a.post) + w(a.next), POST_BWD_REGS, 256, NORM_PARTS);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         parts = sh.ctas;
