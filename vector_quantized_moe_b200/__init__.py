@@ -807,3 +807,43 @@ class MoELayer:
                                             int(bool(renorm)), int(chunk), out.data_ptr(), _dt(out.dtype), aligned,
                                             nbytes, _stream(stream)), "vq_moe_prefill_chunked")
         return out
+
+
+class MoEBlock:
+    """A residual block around a MoE layer, from the residual stream to the residual stream:
+
+        x  = pre(h)                                     (or the x the block before made with its `next` norm)
+        y  = experts(x, router(x)) + sigmoid(shared_gate(x)) * shared expert(x)
+        h' = res_scale * h + out_scale * post(y),   x' = next(h')
+
+    router: x [T, hidden] bf16 -> logits fp32 [T, E]. shared: (gate, up, down) Q4Modules of a SwiGLU expert that every
+    token takes; shared_gate: x -> logits [T, 1], None for 1. post and next may be None."""
+
+    def __init__(self, layer: MoELayer, pre: Norm, router, top_k: int, post: Optional[Norm] = None,
+                 next: Optional[Norm] = None, shared=None, shared_gate=None, renorm: bool = True,
+                 res_scale: float = 1.0, out_scale: float = 1.0):
+        if pre.hidden != layer.hidden or (shared is not None and (shared[0].cols, shared[2].rows) != (layer.hidden,) * 2):
+            _bad("MoEBlock: hidden sizes")
+        self.layer, self.pre, self.post, self.next = layer, pre, post, next
+        self.router, self.shared, self.shared_gate = router, shared, shared_gate
+        self.top_k, self.renorm, self.res_scale, self.out_scale = top_k, renorm, res_scale, out_scale
+
+    def decode(self, h, x=None):
+        """(h', x', router logits) for decode-sized batches; x' is None without `next`."""
+        return self._run(self.layer.decode, h, x)
+
+    def prefill(self, h, x=None):
+        """The same for prefill-sized batches."""
+        return self._run(self.layer.prefill, h, x)
+
+    def _run(self, experts, h, x):
+        if x is None:
+            x = norm_pre(self.pre, h)
+        logits = self.router(x)
+        y = experts(x, logits, self.top_k, self.renorm, out_dtype=_f32)
+        if self.shared is not None:
+            gate, up, down = self.shared
+            s = q4_gemv(down, q4_gemv(gate, x, up))
+            norm_post(s, y, gate=None if self.shared_gate is None else self.shared_gate(x), h_out=y)
+        h, x = norm_post(y, h, self.post, None, self.res_scale, self.out_scale, self.next)
+        return h, x, logits
