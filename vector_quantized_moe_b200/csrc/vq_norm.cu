@@ -17,186 +17,130 @@
 namespace vq {
 namespace {
 
-// ---------------------------------------------------------------- any rows, element by element
-
 // Where a thread's i-th chunk of a row starts, for a row over W warps.
 template <int VEC>
 __device__ __forceinline__ int chunk_at(int i, int tid, int W) { return (tid + i * 32 * W) * VEC; }
 
-template <typename HT, int NV>
-__global__ void __launch_bounds__(1024) vq_norm_pre_scalar_kernel(const NormPreArgs a)
+// ---------------------------------------------------------------- any rows, element by element
+//
+// Rows off the 16-byte boundaries (odd widths, windows of wider arrays): a
+// warp's loads and stores are contiguous elements, a row's fp32 values wait in
+// shared memory between the passes, and several CTAs on an SM overlap.
+
+template <typename HT>
+__global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_scalar_kernel(const NormPreArgs a)
 {
-    constexpr int VEC = 1;
     __shared__ RowSum<1> rs;
+    extern __shared__ float rows_f32[];
     grid_dep_launch();
     grid_dep_wait();
     const RowTeam team(a.W);
-    const int W = team.W, tid = team.tid;
-    const long row = (long)blockIdx.x * team.R + team.rg;
-    if (row >= a.T)   // only in CTAs of one-warp rows, which never meet at a barrier
-        return;
-    const HT *h = static_cast<const HT *>(a.h) + row * a.h_ld;
-    Chunk<HT, VEC> hc[NV];
-    AnyChunk<VEC> wc[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = chunk_at<VEC>(i, tid, W);
-        if (c < a.H)
-            hc[i].load(h + c);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = chunk_at<VEC>(i, tid, W);
-        if (c < a.H)
-            wc[i].load(a.n.weight, a.n.dtype, c);
-    }
-    float ss[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (chunk_at<VEC>(i, tid, W) < a.H) {
-            float v[VEC];
-            hc[i].get(v);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                ss[0] = fmaf(v[j], v[j], ss[0]);
-        }
-    }
+    const int step = 32 * team.W;
+    float *u = rows_f32 + team.rg * a.H;
     int turn = 0;
-    row_sum(ss, rs, team, turn);
-    const float r = rsqrtf(ss[0] * a.inv_h + a.n.eps);
-    uint16_t *x = a.x + row * a.x_ld;
+    for (long row = (long)blockIdx.x * team.R + team.rg; row < a.T; row += (long)gridDim.x * team.R) {
+        const HT *h = static_cast<const HT *>(a.h) + row * a.h_ld;
+        float ss[1] = {0.f};
+        for (int e0 = team.tid; e0 < a.H; e0 += BATCH * step) {
+            float v[BATCH];
+            batch(v, h, e0, step, a.H);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = chunk_at<VEC>(i, tid, W);
-        if (c < a.H) {
-            float v[VEC], w[VEC];
-            hc[i].get(v);
-            wc[i].get(w, a.n.dtype);
+            for (int i = 0; i < BATCH; ++i)
+                if (e0 + i * step < a.H) {
+                    u[e0 + i * step] = v[i];
+                    ss[0] = fmaf(v[i], v[i], ss[0]);
+                }
+        }
+        row_sum(ss, rs, team, turn);
+        const float r = rsqrtf(ss[0] * a.inv_h + a.n.eps);
+        uint16_t *x = a.x + row * a.x_ld;
+        for (int e0 = team.tid; e0 < a.H; e0 += BATCH * step) {
+            float w[BATCH], v[BATCH];
+            batch_any(w, a.n.weight, a.n.dtype, 0, e0, step, a.H);
+            batch(v, u, e0, step, a.H);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                v[j] = v[j] * r * (w[j] + a.n.offset);
-            Chunk<uint16_t, VEC> o;
-            o.set(v);
-            o.store(x + c);
+            for (int i = 0; i < BATCH; ++i)
+                if (e0 + i * step < a.H)
+                    put(x[e0 + i * step], v[i] * r * (w[i] + a.n.offset));
         }
     }
 }
 
-template <typename YT, typename HT, int NV>
-__global__ void __launch_bounds__(1024) vq_norm_post_scalar_kernel(const NormPostArgs a)
+template <typename YT, typename HT>
+__global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_scalar_kernel(const NormPostArgs a)
 {
-    constexpr int VEC = 1;
     __shared__ RowSum<1> rs;
+    extern __shared__ float rows_f32[];
     grid_dep_launch();
     grid_dep_wait();
     const RowTeam team(a.W);
-    const int W = team.W, tid = team.tid;
-    const long row = (long)blockIdx.x * team.R + team.rg;
-    if (row >= a.T)
-        return;
-    const YT *y = static_cast<const YT *>(a.y) + row * a.y_ld;
-    const HT *h = static_cast<const HT *>(a.h) + row * a.h_ld;
-    Chunk<YT, VEC> yc[NV];
-    Chunk<HT, VEC> hc[NV];
-    AnyChunk<VEC> w1[NV], w2[NV], zc[NV];
-    float gate = 1.f;
-    if (a.gate_mode == GATE_TOKEN) {
-        AnyChunk<1> z;
-        float v[1];
-        z.load(a.gate, a.gate_dtype, row * a.gate_ld);
-        z.get(v, a.gate_dtype);
-        gate = sigmoid(v[0]);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = chunk_at<VEC>(i, tid, W);
-        if (c < a.H) {
-            yc[i].load(y + c);
-            hc[i].load(h + c);
-            if (a.gate_mode == GATE_CHANNEL)
-                zc[i].load(a.gate, a.gate_dtype, row * a.gate_ld + c);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = chunk_at<VEC>(i, tid, W);
-        if (c < a.H) {
-            if (a.post.weight)
-                w1[i].load(a.post.weight, a.post.dtype, c);
-            if (a.next.weight)
-                w2[i].load(a.next.weight, a.next.dtype, c);
-        }
-    }
+    const int step = 32 * team.W;
+    float *u = rows_f32 + team.rg * a.H;
     int turn = 0;
-    float r1 = 1.f;
-    if (a.post.weight) {
-        float ss[1] = {0.f};
+    for (long row = (long)blockIdx.x * team.R + team.rg; row < a.T; row += (long)gridDim.x * team.R) {
+        const YT *y = static_cast<const YT *>(a.y) + row * a.y_ld;
+        const HT *h = static_cast<const HT *>(a.h) + row * a.h_ld;
+        HT *ho = static_cast<HT *>(a.h_out) + row * a.ho_ld;
+        float f = a.out_scale;   // the branch's factor, but for the weight and a channel's gate
+        if (a.gate_mode == GATE_TOKEN)
+            f *= sigmoid(weight_at(a.gate, a.gate_dtype, row * a.gate_ld));
+        if (a.post.weight) {
+            float ss[1] = {0.f};
+            for (int e0 = team.tid; e0 < a.H; e0 += BATCH * step) {
+                float v[BATCH];
+                batch(v, y, e0, step, a.H);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (chunk_at<VEC>(i, tid, W) < a.H) {
-                float v[VEC];
-                yc[i].get(v);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                    ss[0] = fmaf(v[j], v[j], ss[0]);
+                for (int i = 0; i < BATCH; ++i)
+                    if (e0 + i * step < a.H) {
+                        u[e0 + i * step] = v[i];
+                        ss[0] = fmaf(v[i], v[i], ss[0]);
+                    }
             }
-        row_sum(ss, rs, team, turn);
-        r1 = rsqrtf(ss[0] * a.inv_h + a.post.eps);
-    }
-    float ss[1] = {0.f};
-    HT *ho = static_cast<HT *>(a.h_out) + row * a.ho_ld;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = chunk_at<VEC>(i, tid, W);
-        if (c < a.H) {
-            float u[VEC], v[VEC], t[VEC];
-            yc[i].get(u);
-            hc[i].get(v);
-            if (a.post.weight) {
-                w1[i].get(t, a.post.dtype);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                    u[j] = u[j] * r1 * (t[j] + a.post.offset);
-            }
-            if (a.gate_mode == GATE_CHANNEL) {
-                zc[i].get(t, a.gate_dtype);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                    u[j] *= sigmoid(t[j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                    u[j] *= gate;
-            }
-#pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                v[j] = a.res_scale * v[j] + a.out_scale * u[j];
-            hc[i].set(v);   // the row as stored: what the next norm sees
-            hc[i].store(ho + c);
-            hc[i].get(v);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                ss[0] = fmaf(v[j], v[j], ss[0]);
+            row_sum(ss, rs, team, turn);
+            f *= rsqrtf(ss[0] * a.inv_h + a.post.eps);
         }
-    }
-    if (!a.next.weight)
-        return;
-    row_sum(ss, rs, team, turn);
-    const float r2 = rsqrtf(ss[0] * a.inv_h + a.next.eps);
-    uint16_t *x = a.x + row * a.x_ld;
+        float ss[1] = {0.f};
+        for (int e0 = team.tid; e0 < a.H; e0 += BATCH * step) {
+            float v[BATCH], w[BATCH], z[BATCH], r[BATCH];
+            batch(r, h, e0, step, a.H);
+            if (a.post.weight) {
+                batch(v, u, e0, step, a.H);
+                batch_any(w, a.post.weight, a.post.dtype, 0, e0, step, a.H);
+            } else {
+                batch(v, y, e0, step, a.H);
+            }
+            if (a.gate_mode == GATE_CHANNEL)
+                batch_any(z, a.gate, a.gate_dtype, row * a.gate_ld, e0, step, a.H);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = chunk_at<VEC>(i, tid, W);
-        if (c < a.H) {
-            float v[VEC], w[VEC];
-            hc[i].get(v);
-            w2[i].get(w, a.next.dtype);
+            for (int i = 0; i < BATCH; ++i) {
+                const int e = e0 + i * step;
+                if (e >= a.H)
+                    break;
+                v[i] *= f;
+                if (a.post.weight)
+                    v[i] *= w[i] + a.post.offset;
+                if (a.gate_mode == GATE_CHANNEL)
+                    v[i] *= sigmoid(z[i]);
+                HT o;
+                put(o, fmaf(a.res_scale, r[i], v[i]));
+                ho[e] = o;   // the row as stored: what the next norm sees
+                u[e] = element(o);
+                ss[0] = fmaf(element(o), element(o), ss[0]);
+            }
+        }
+        if (!a.next.weight)
+            continue;
+        row_sum(ss, rs, team, turn);
+        const float r = rsqrtf(ss[0] * a.inv_h + a.next.eps);
+        uint16_t *x = a.x + row * a.x_ld;
+        for (int e0 = team.tid; e0 < a.H; e0 += BATCH * step) {
+            float w[BATCH], v[BATCH];
+            batch_any(w, a.next.weight, a.next.dtype, 0, e0, step, a.H);
+            batch(v, u, e0, step, a.H);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                v[j] = v[j] * r2 * (w[j] + a.next.offset);
-            Chunk<uint16_t, VEC> o;
-            o.set(v);
-            o.store(x + c);
+            for (int i = 0; i < BATCH; ++i)
+                if (e0 + i * step < a.H)
+                    put(x[e0 + i * step], v[i] * r * (w[i] + a.next.offset));
         }
     }
 }
@@ -417,20 +361,6 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_kernel(const NormPos
     }
 }
 
-// Scalar rows: as many threads as elements, up to 16 elements each.
-struct ScalarShape {
-    int W, R, nv;
-};
-
-ScalarShape scalar_shape(int H)
-{
-    ScalarShape s;
-    s.nv = H <= 1024 ? 1 : H <= 4096 ? 4 : 16;
-    s.W = ((H + s.nv - 1) / s.nv + 31) / 32;
-    s.R = s.W == 1 ? 4 : 1;
-    return s;
-}
-
 constexpr int PRE_REGS[4] = {48, 64, 80, 104}, POST_REGS[4] = {64, 88, 112, 128};
 
 template <auto K, typename Args>
@@ -452,12 +382,9 @@ cudaError_t pre_launch(NormPreArgs a, bool vec8, cudaStream_t s)
         default: return rows<vq_norm_pre_kernel<HT, 4>>(sh, s, a);
         }
     }
-    const ScalarShape sc = scalar_shape(a.H);
+    const NormShape sc = scalar_shape(a.H, a.T, 1, 0);
     a.W = sc.W;
-    const dim3 grid((unsigned)(((long)a.T + sc.R - 1) / sc.R)), block(32 * sc.W * sc.R);
-    return sc.nv == 1   ? launch_after(vq_norm_pre_scalar_kernel<HT, 1>, grid, block, 0, s, a)
-           : sc.nv == 4 ? launch_after(vq_norm_pre_scalar_kernel<HT, 4>, grid, block, 0, s, a)
-                        : launch_after(vq_norm_pre_scalar_kernel<HT, 16>, grid, block, 0, s, a);
+    return launch_smem<vq_norm_pre_scalar_kernel<HT>, SCALAR_SMEM>(dim3(sc.ctas), dim3(32 * sc.W * sc.R), sc.smem, s, a);
 }
 
 template <typename YT, typename HT>
@@ -474,15 +401,26 @@ cudaError_t post_launch(NormPostArgs a, bool vec8, cudaStream_t s)
         default: return rows<vq_norm_post_kernel<YT, HT, 4>>(sh, s, a);
         }
     }
-    const ScalarShape sc = scalar_shape(a.H);
+    const NormShape sc = scalar_shape(a.H, a.T, 1, 0);
     a.W = sc.W;
-    const dim3 grid((unsigned)(((long)a.T + sc.R - 1) / sc.R)), block(32 * sc.W * sc.R);
-    return sc.nv == 1   ? launch_after(vq_norm_post_scalar_kernel<YT, HT, 1>, grid, block, 0, s, a)
-           : sc.nv == 4 ? launch_after(vq_norm_post_scalar_kernel<YT, HT, 4>, grid, block, 0, s, a)
-                        : launch_after(vq_norm_post_scalar_kernel<YT, HT, 16>, grid, block, 0, s, a);
+    return launch_smem<vq_norm_post_scalar_kernel<YT, HT>, SCALAR_SMEM>(dim3(sc.ctas), dim3(32 * sc.W * sc.R), sc.smem, s, a);
 }
 
 }  // namespace
+
+NormShape scalar_shape(int H, int T, int floats, int max_ctas)
+{
+    NormShape s{};
+    s.W = H <= 128 ? 1 : H <= 256 ? 2 : H <= 512 ? 4 : H <= 8192 ? 8 : 16;
+    s.R = std::max(1, 8 / s.W);
+    s.smem = (size_t)s.R * H * floats * sizeof(float);
+    const int per_sm = (int)std::max<size_t>(1, std::min<size_t>(s.W == 16 ? 3 : 6, SCALAR_SMEM / (s.smem + 2048)));
+    long ctas = std::min(((long)T + s.R - 1) / s.R, 148L * per_sm);
+    if (max_ctas)
+        ctas = std::min<long>(ctas, max_ctas);
+    s.ctas = (int)std::max(1L, ctas);
+    return s;
+}
 
 NormShape norm_shape(int H, int T, int bytes, int fixed, const int (&regs)[4], int threads, int max_ctas)
 {

@@ -1,6 +1,7 @@
 // Arguments of the block-norm kernels (vq_norm.cu, vq_norm_bwd.cu).
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -20,6 +21,33 @@ struct NormDev {
 enum { GATE_NONE = 0, GATE_TOKEN = 1, GATE_CHANNEL = 2 };
 
 #ifdef __CUDACC__
+// Single elements: fp32 or bf16, and of a type known at run time.
+__device__ __forceinline__ float element(float v) { return v; }
+__device__ __forceinline__ float element(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ void put(float &o, float v) { o = v; }
+__device__ __forceinline__ void put(uint16_t &o, float v) { o = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+// A batch of a thread's elements e, e + step, ...: loaded before any of the batch is stored, since an output may be
+// the input itself and the compiler then keeps every load behind the stores before it.
+constexpr int BATCH = 4;
+template <typename T>
+__device__ __forceinline__ void batch(float (&v)[BATCH], const T *p, int e, int step, int H)
+{
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+        v[i] = e + i * step < H ? element(p[e + i * step]) : 0.f;
+}
+__device__ __forceinline__ void batch_any(float (&v)[BATCH], const void *p, int dtype, long at, int e, int step, int H)
+{
+    if (dtype == VQ_F32)
+        batch(v, static_cast<const float *>(p) + at, e, step, H);
+    else
+        batch(v, static_cast<const uint16_t *>(p) + at, e, step, H);
+}
+__device__ __forceinline__ float weight_at(const void *p, int dtype, long i)
+{
+    return dtype == VQ_F32 ? static_cast<const float *>(p)[i] : element(static_cast<const uint16_t *>(p)[i]);
+}
+
 // The fast exponential and reciprocal: their error is a few 2^-24 times max(1, |z|), that of a rounding of z.
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
@@ -87,6 +115,11 @@ constexpr int NORM_SMEM = 222 * 1024;      // shared memory of an SM given to th
 // bytes: of input an element copied ahead; fixed: bytes an element kept for the whole launch; regs: registers a
 // thread at nv chunks (regs[nv - 1]); threads: a row's threads when rows stream; max_ctas: 0, or the most CTAs.
 NormShape norm_shape(int H, int T, int bytes, int fixed, const int (&regs)[4], int threads, int max_ctas);
+
+// The same for the element-by-element kernels: about 256 threads a CTA, `floats` fp32 values an element in shared
+// memory for each of its rows side by side.
+constexpr int SCALAR_SMEM = 224 * 1024;
+NormShape scalar_shape(int H, int T, int floats, int max_ctas);
 
 // vec8: every row (pointers and strides) on 16-byte boundaries and H a multiple of 8.
 cudaError_t launch_norm_pre(const NormPreArgs &a, int h_dtype, bool vec8, cudaStream_t s);

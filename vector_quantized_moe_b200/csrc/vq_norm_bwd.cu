@@ -20,293 +20,203 @@ constexpr int NORM_PARTS = 592;     // most partial rows: 4 CTAs on each of 148 
 template <int VEC>
 __device__ __forceinline__ int chunk_at(int i, int tid, int W) { return (tid + i * 32 * W) * VEC; }
 
-template <typename HT, int NV>
+// ---------------------------------------------------------------- any rows, element by element
+//
+// A thread's columns are the same in every row, so the weight gradients' sums
+// wait in shared memory without a barrier. Arrays are read again in each pass
+// (from L1 or L2).
+
+// A CTA's partial row: its side-by-side rows' sums (the first floats of each row's share) added in order.
+__device__ __forceinline__ void write_part_scalar(float *part, const float *acc, int share, int R, int H)
+{
+    __syncthreads();
+    for (int e = threadIdx.x; e < H; e += blockDim.x) {
+        float v = acc[e];
+        for (int r = 1; r < R; ++r)
+            v += acc[(size_t)r * share + e];
+        part[(long)blockIdx.x * H + e] = v;
+    }
+}
+
+template <typename HT>
 __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_bwd_scalar_kernel(const NormPreBwdArgs a)
 {
-    constexpr int VEC = 1;
     __shared__ RowSum<2> rs;
+    extern __shared__ float sums[];   // [R][H]
     grid_dep_launch();
     grid_dep_wait();
     const RowTeam team(a.W);
-    const int W = team.W, tid = team.tid, R = team.R;
-    const int slot = blockIdx.x * R + team.rg;
-    float acc[NV][VEC];
-    AnyChunk<VEC> wc[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = chunk_at<VEC>(i, tid, W);
-        if (c < a.H)
-            wc[i].load(a.n.weight, a.n.dtype, c);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-            acc[i][j] = 0.f;
-    }
+    const int step = 32 * team.W;
+    float *acc = sums + team.rg * a.H;
+    for (int e = team.tid; e < a.H; e += step)
+        acc[e] = 0.f;
     int turn = 0;
-    // one row of W > 1 warps per CTA: all its warps take the same trips; rows of one warp meet at no barrier
-    for (long row = slot; row < a.T; row += (long)gridDim.x * R) {
+    for (long row = (long)blockIdx.x * team.R + team.rg; row < a.T; row += (long)gridDim.x * team.R) {
         const HT *h = static_cast<const HT *>(a.h) + row * a.h_ld;
         const HT *dres = static_cast<const HT *>(a.dres) + row * a.dres_ld;
         const uint16_t *dx = a.dx + row * a.dx_ld;
         HT *dh = static_cast<HT *>(a.dh) + row * a.dh_ld;
-        Chunk<HT, VEC> hc[NV], rc[NV];
-        Chunk<uint16_t, VEC> dc[NV];
+        float q[2] = {0.f, 0.f};   // |h|^2, sum g h
+        for (int e0 = team.tid; e0 < a.H; e0 += BATCH * step) {
+            float v[BATCH], d[BATCH], w[BATCH];
+            batch(v, h, e0, step, a.H);
+            batch(d, dx, e0, step, a.H);
+            batch_any(w, a.n.weight, a.n.dtype, 0, e0, step, a.H);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = chunk_at<VEC>(i, tid, W);
-            if (c < a.H) {
-                hc[i].load(h + c);
-                dc[i].load(dx + c);
-                if (a.dres)
-                    rc[i].load(dres + c);
+            for (int i = 0; i < BATCH; ++i) {   // elements past the row are zeros
+                q[0] = fmaf(v[i], v[i], q[0]);
+                q[1] = fmaf(d[i] * (w[i] + a.n.offset), v[i], q[1]);
             }
         }
-        float s[2] = {0.f, 0.f};
+        row_sum(q, rs, team, turn);
+        const float r = rsqrtf(q[0] * a.inv_h + a.n.eps);
+        const float rm = r * (r * (q[1] * a.inv_h));   // r mean(g v^)
+        for (int e0 = team.tid; e0 < a.H; e0 += BATCH * step) {
+            float v[BATCH], d[BATCH], w[BATCH], o[BATCH];
+            batch(v, h, e0, step, a.H);
+            batch(d, dx, e0, step, a.H);
+            batch_any(w, a.n.weight, a.n.dtype, 0, e0, step, a.H);
+            if (a.dres)
+                batch(o, dres, e0, step, a.H);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (chunk_at<VEC>(i, tid, W) < a.H) {
-                float v[VEC], d[VEC], w[VEC];
-                hc[i].get(v);
-                dc[i].get(d);
-                wc[i].get(w, a.n.dtype);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    s[0] = fmaf(v[j], v[j], s[0]);
-                    s[1] = fmaf(d[j] * (w[j] + a.n.offset), v[j], s[1]);
-                }
-            }
-        row_sum(s, rs, team, turn);
-        const float r = rsqrtf(s[0] * a.inv_h + a.n.eps);
-        const float m = r * (s[1] * a.inv_h);   // mean(g v^)
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = chunk_at<VEC>(i, tid, W);
-            if (c < a.H) {
-                float v[VEC], d[VEC], w[VEC], o[VEC];
-                hc[i].get(v);
-                dc[i].get(d);
-                wc[i].get(w, a.n.dtype);
-                if (a.dres)
-                    rc[i].get(o);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float n = v[j] * r;
-                    acc[i][j] = fmaf(d[j], n, acc[i][j]);
-                    const float t = r * (d[j] * (w[j] + a.n.offset) - n * m);
-                    o[j] = a.dres ? o[j] + t : t;
-                }
-                Chunk<HT, VEC> oc;
-                oc.set(o);
-                oc.store(dh + c);
+            for (int i = 0; i < BATCH; ++i) {
+                const int e = e0 + i * step;
+                if (e >= a.H)
+                    break;
+                const float n = v[i] * r, t = fmaf(-n, rm, r * (d[i] * (w[i] + a.n.offset)));
+                acc[e] = fmaf(d[i], n, acc[e]);
+                put(dh[e], a.dres ? o[i] + t : t);
             }
         }
     }
-    if (!a.part)
-        return;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = chunk_at<VEC>(i, tid, W);
-        if (c < a.H)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                a.part[(long)slot * a.H + c + j] = acc[i][j];
-    }
+    if (a.part)
+        write_part_scalar(a.part, sums, a.H, team.R, a.H);
 }
 
-template <typename YT, typename HT, int NV>
+template <typename YT, typename HT>
 __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_scalar_kernel(const NormPostBwdArgs a)
 {
-    constexpr int VEC = 1;
     __shared__ RowSum<3> rs;
+    extern __shared__ float sums[];   // [R][3][H]: the two weight gradients, and a row's values between the passes
     grid_dep_launch();
     grid_dep_wait();
     const RowTeam team(a.W);
-    const int W = team.W, tid = team.tid, R = team.R;
-    const int slot = blockIdx.x * R + team.rg;
+    const int step = 32 * team.W;
     const bool post = a.post.weight != nullptr, next = a.next.weight != nullptr;
-    float acc1[NV][VEC], acc2[NV][VEC];
-    AnyChunk<VEC> w1[NV], w2[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = chunk_at<VEC>(i, tid, W);
-        if (c < a.H) {
-            if (post)
-                w1[i].load(a.post.weight, a.post.dtype, c);
-            if (next)
-                w2[i].load(a.next.weight, a.next.dtype, c);
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-            acc1[i][j] = acc2[i][j] = 0.f;
-    }
+    float *acc1 = sums + (size_t)team.rg * 3 * a.H, *acc2 = acc1 + a.H, *g = acc2 + a.H;
+    for (int e = team.tid; e < a.H; e += step)
+        acc1[e] = acc2[e] = 0.f;
     int turn = 0;
-    for (long row = slot; row < a.T; row += (long)gridDim.x * R) {
+    for (long row = (long)blockIdx.x * team.R + team.rg; row < a.T; row += (long)gridDim.x * team.R) {
         const YT *y = static_cast<const YT *>(a.y) + row * a.y_ld;
         const HT *h = static_cast<const HT *>(a.h) + row * a.h_ld;
         const HT *dho = static_cast<const HT *>(a.dho) + row * a.dho_ld;
         const uint16_t *dx = a.dx + row * a.dx_ld;
-        Chunk<YT, VEC> yc[NV];
-        Chunk<HT, VEC> hc[NV], gc[NV];
-        Chunk<uint16_t, VEC> dc[NV];
-        AnyChunk<VEC> zc[NV];
+        YT *dy = static_cast<YT *>(a.dy) + row * a.dy_ld;
+        HT *dh = static_cast<HT *>(a.dh) + row * a.dh_ld;
         float on = 1.f, off = 0.f;   // sigmoid(z), 1 - sigmoid(z)
-        if (a.gate_mode == GATE_TOKEN) {
-            AnyChunk<1> z;
-            float v[1];
-            z.load(a.gate, a.gate_dtype, row * a.gate_ld);
-            z.get(v, a.gate_dtype);
-            on = sigmoid(v[0]);
-            off = sigmoid(-v[0]);
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = chunk_at<VEC>(i, tid, W);
-            if (c < a.H) {
-                yc[i].load(y + c);
+        if (a.gate_mode == GATE_TOKEN)
+            sigmoids(weight_at(a.gate, a.gate_dtype, row * a.gate_ld), on, off);
+        float q[3] = {0.f, 0.f, 0.f};   // |h'|^2, sum g h' of the next norm, |y|^2
+        if (next || post) {
+            for (int e0 = team.tid; e0 < a.H; e0 += BATCH * step) {
+                float v[BATCH], d[BATCH], w[BATCH];
                 if (next) {
-                    hc[i].load(h + c);
-                    dc[i].load(dx + c);
-                }
-                if (a.dho)
-                    gc[i].load(dho + c);
-                if (a.gate_mode == GATE_CHANNEL)
-                    zc[i].load(a.gate, a.gate_dtype, row * a.gate_ld + c);
-            }
-        }
-        // the sums that need nothing but the inputs: |h'|^2, sum g h' of the next norm, |y|^2
-        float s[3] = {0.f, 0.f, 0.f};
+                    batch(v, h, e0, step, a.H);
+                    batch(d, dx, e0, step, a.H);
+                    batch_any(w, a.next.weight, a.next.dtype, 0, e0, step, a.H);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (chunk_at<VEC>(i, tid, W) < a.H) {
-                float v[VEC], d[VEC], w[VEC];
-                if (next) {
-                    hc[i].get(v);
-                    dc[i].get(d);
-                    w2[i].get(w, a.next.dtype);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        s[0] = fmaf(v[j], v[j], s[0]);
-                        s[1] = fmaf(d[j] * (w[j] + a.next.offset), v[j], s[1]);
+                    for (int i = 0; i < BATCH; ++i) {   // elements past the row are zeros
+                        q[0] = fmaf(v[i], v[i], q[0]);
+                        q[1] = fmaf(d[i] * (w[i] + a.next.offset), v[i], q[1]);
                     }
                 }
                 if (post) {
-                    yc[i].get(v);
+                    batch(v, y, e0, step, a.H);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j)
-                        s[2] = fmaf(v[j], v[j], s[2]);
+                    for (int i = 0; i < BATCH; ++i)
+                        q[2] = fmaf(v[i], v[i], q[2]);
                 }
             }
-        if (next || post)
-            row_sum(s, rs, team, turn);
-        const float r2 = rsqrtf(s[0] * a.inv_h + a.next.eps), m2 = r2 * (s[1] * a.inv_h);
-        const float r1 = post ? rsqrtf(s[2] * a.inv_h + a.post.eps) : 1.f;
-        float dH[NV][VEC];
-        float q[2] = {0.f, 0.f};   // sum g y of the post norm, sum dv u of a token's gate
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = chunk_at<VEC>(i, tid, W);
-            if (c < a.H) {
-                float v[VEC], d[VEC], w[VEC];
-                if (a.dho)
-                    gc[i].get(dH[i]);
-                else
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j)
-                        dH[i][j] = 0.f;
-                if (next) {
-                    hc[i].get(v);
-                    dc[i].get(d);
-                    w2[i].get(w, a.next.dtype);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const float n = v[j] * r2;
-                        acc2[i][j] = fmaf(d[j], n, acc2[i][j]);
-                        dH[i][j] += r2 * (d[j] * (w[j] + a.next.offset) - n * m2);
-                    }
-                }
-                if (a.dh) {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j)
-                        d[j] = a.res_scale * dH[i][j];
-                    Chunk<HT, VEC> oc;
-                    oc.set(d);
-                    oc.store(static_cast<HT *>(a.dh) + row * a.dh_ld + c);
-                }
-                yc[i].get(v);
-                if (post)
-                    w1[i].get(w, a.post.dtype);
-                float z[VEC];
-                if (a.gate_mode == GATE_CHANNEL)
-                    zc[i].get(z, a.gate_dtype);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    float du = a.out_scale * dH[i][j];                                    // dv
-                    const float wj = post ? w[j] + a.post.offset : 1.f;
-                    const float n = v[j] * r1;
-                    q[1] = fmaf(du, n * wj, q[1]);                                        // dv u
-                    if (a.gate_mode == GATE_CHANNEL) {
-                        const float so = sigmoid(z[j]);
-                        z[j] = du * (n * wj) * so * sigmoid(-z[j]);
-                        du *= so;
-                    } else {
-                        du *= on;
-                    }
-                    acc1[i][j] = fmaf(du, n, acc1[i][j]);
-                    du *= wj;                                                             // g
-                    q[0] = fmaf(du, v[j], q[0]);
-                    dH[i][j] = du;
-                }
-                if (a.gate_mode == GATE_CHANNEL && a.dgate) {
-                    const long at = row * a.dgate_ld + c;
-                    if (a.gate_dtype == VQ_F32) {
-                        Chunk<float, VEC> oc;
-                        oc.set(z);
-                        oc.store(static_cast<float *>(a.dgate) + at);
-                    } else {
-                        Chunk<uint16_t, VEC> oc;
-                        oc.set(z);
-                        oc.store(static_cast<uint16_t *>(a.dgate) + at);
-                    }
-                }
-            }
-        }
-        if (post || (a.gate_mode == GATE_TOKEN && a.dgate))
             row_sum(q, rs, team, turn);
-        if (a.gate_mode == GATE_TOKEN && a.dgate && tid == 0) {
-            const float dz = q[1] * on * off;
-            const long at = row * a.dgate_ld;
+        }
+        const float r2 = rsqrtf(q[0] * a.inv_h + a.next.eps), rm2 = r2 * (r2 * (q[1] * a.inv_h));
+        const float r1 = post ? rsqrtf(q[2] * a.inv_h + a.post.eps) : 1.f;
+        float t[2] = {0.f, 0.f};   // sums: g y^ of the post norm, dv u of a token's gate
+        for (int e0 = team.tid; e0 < a.H; e0 += BATCH * step) {
+            float dH[BATCH], v[BATCH], w[BATCH], z[BATCH], hv[BATCH], d[BATCH], w2[BATCH];
+            batch(v, y, e0, step, a.H);
+            if (a.dho)
+                batch(dH, dho, e0, step, a.H);
+            if (next) {
+                batch(hv, h, e0, step, a.H);
+                batch(d, dx, e0, step, a.H);
+                batch_any(w2, a.next.weight, a.next.dtype, 0, e0, step, a.H);
+            }
+            if (post)
+                batch_any(w, a.post.weight, a.post.dtype, 0, e0, step, a.H);
+            if (a.gate_mode == GATE_CHANNEL)
+                batch_any(z, a.gate, a.gate_dtype, row * a.gate_ld, e0, step, a.H);
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int e = e0 + i * step;
+                if (e >= a.H)
+                    break;
+                float s = a.dho ? dH[i] : 0.f;
+                if (next) {
+                    const float n = hv[i] * r2;
+                    acc2[e] = fmaf(d[i], n, acc2[e]);
+                    s += fmaf(-n, rm2, r2 * (d[i] * (w2[i] + a.next.offset)));
+                }
+                if (a.dh)
+                    put(dh[e], a.res_scale * s);
+                const float dv = a.out_scale * s, n = v[i] * r1, wj = post ? w[i] + a.post.offset : 1.f;
+                float zon = on, zoff;
+                if (a.gate_mode == GATE_CHANNEL) {
+                    sigmoids(z[i], zon, zoff);
+                    if (a.dgate) {
+                        const float dz = dv * (n * wj) * zon * zoff;
+                        const long to = row * a.dgate_ld + e;
+                        if (a.gate_dtype == VQ_F32)
+                            static_cast<float *>(a.dgate)[to] = dz;
+                        else
+                            put(static_cast<uint16_t *>(a.dgate)[to], dz);
+                    }
+                }
+                const float du = dv * zon;
+                acc1[e] = fmaf(du, n, acc1[e]);
+                g[e] = du * wj;
+                t[0] = fmaf(du * wj, n, t[0]);
+                t[1] = fmaf(dv, n * wj, t[1]);
+            }
+        }
+        const bool token = a.gate_mode == GATE_TOKEN && a.dgate;
+        if (post || token)
+            row_sum(t, rs, team, turn);
+        if (token && team.tid == 0) {
+            const float dz = t[1] * on * off;
+            const long to = row * a.dgate_ld;
             if (a.gate_dtype == VQ_F32)
-                static_cast<float *>(a.dgate)[at] = dz;
+                static_cast<float *>(a.dgate)[to] = dz;
             else
-                static_cast<uint16_t *>(a.dgate)[at] = f32_to_bf16_bits(dz);
+                put(static_cast<uint16_t *>(a.dgate)[to], dz);
         }
-        const float m1 = r1 * (q[0] * a.inv_h);
+        const float rm1 = r1 * (t[0] * a.inv_h);   // r1 mean(g y^)
+        for (int e0 = team.tid; e0 < a.H; e0 += BATCH * step) {
+            float v[BATCH], o[BATCH];
+            batch(o, g, e0, step, a.H);
+            if (post)
+                batch(v, y, e0, step, a.H);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = chunk_at<VEC>(i, tid, W);
-            if (c < a.H) {
-                float v[VEC];
-                yc[i].get(v);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                    v[j] = post ? r1 * (dH[i][j] - v[j] * r1 * m1) : dH[i][j];
-                Chunk<YT, VEC> oc;
-                oc.set(v);
-                oc.store(static_cast<YT *>(a.dy) + row * a.dy_ld + c);
-            }
+            for (int i = 0; i < BATCH; ++i)
+                if (e0 + i * step < a.H)
+                    put(dy[e0 + i * step], post ? fmaf(-(v[i] * r1), rm1, r1 * o[i]) : o[i]);
         }
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = chunk_at<VEC>(i, tid, W);
-        if (c < a.H)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                if (a.part1)
-                    a.part1[(long)slot * a.H + c + j] = acc1[i][j];
-                if (a.part2)
-                    a.part2[(long)slot * a.H + c + j] = acc2[i][j];
-            }
-    }
+    if (a.part1)
+        write_part_scalar(a.part1, sums, 3 * a.H, team.R, a.H);
+    if (a.part2)
+        write_part_scalar(a.part2, sums + a.H, 3 * a.H, team.R, a.H);
 }
 
 // ---------------------------------------------------------------- rows on 16-byte boundaries, copied ahead
@@ -727,17 +637,6 @@ __global__ void __launch_bounds__(256) vq_norm_dw_kernel(const float *p1, float 
     }
 }
 
-// Scalar rows: up to 32 elements a thread.
-NormShape scalar_shape(int H, int T)
-{
-    NormShape s{};
-    s.nv = H <= ROW_THREADS ? 1 : H <= 8 * ROW_THREADS ? 8 : 32;
-    s.W = ((H + s.nv - 1) / s.nv + 31) / 32;
-    s.R = s.W == 1 ? 4 : 1;
-    s.ctas = (int)std::max(1L, std::min(((long)T + s.R - 1) / s.R, (long)NORM_PARTS / s.R));
-    return s;
-}
-
 cudaError_t finish(int parts, int H, const float *p1, float *d1, const float *p2, float *d2, cudaStream_t s)
 {
     if (!d1 && !d2)
@@ -768,13 +667,10 @@ cudaError_t pre_bwd(NormPreBwdArgs a, bool vec8, int &parts, cudaStream_t s)
         default: return rows<vq_norm_pre_bwd_kernel<HT, 4>>(sh, s, a);
         }
     }
-    sh = scalar_shape(a.H, a.T);
+    sh = scalar_shape(a.H, a.T, 1, NORM_PARTS);
     a.W = sh.W;
-    parts = sh.ctas * sh.R;
-    const dim3 grid(sh.ctas), block(32 * sh.W * sh.R);
-    return sh.nv == 1   ? launch_after(vq_norm_pre_bwd_scalar_kernel<HT, 1>, grid, block, 0, s, a)
-           : sh.nv == 8 ? launch_after(vq_norm_pre_bwd_scalar_kernel<HT, 8>, grid, block, 0, s, a)
-                        : launch_after(vq_norm_pre_bwd_scalar_kernel<HT, 32>, grid, block, 0, s, a);
+    parts = sh.ctas;
+    return launch_smem<vq_norm_pre_bwd_scalar_kernel<HT>, SCALAR_SMEM>(dim3(sh.ctas), dim3(32 * sh.W * sh.R), sh.smem, s, a);
 }
 
 template <typename YT, typename HT>
@@ -794,21 +690,18 @@ cudaError_t post_bwd(NormPostBwdArgs a, bool vec8, int &parts, cudaStream_t s)
         default: return rows<vq_norm_post_bwd_kernel<YT, HT, 4>>(sh, s, a);
         }
     }
-    sh = scalar_shape(a.H, a.T);
+    sh = scalar_shape(a.H, a.T, 3, NORM_PARTS);
     a.W = sh.W;
-    parts = sh.ctas * sh.R;
-    const dim3 grid(sh.ctas), block(32 * sh.W * sh.R);
-    return sh.nv == 1   ? launch_after(vq_norm_post_bwd_scalar_kernel<YT, HT, 1>, grid, block, 0, s, a)
-           : sh.nv == 8 ? launch_after(vq_norm_post_bwd_scalar_kernel<YT, HT, 8>, grid, block, 0, s, a)
-                        : launch_after(vq_norm_post_bwd_scalar_kernel<YT, HT, 32>, grid, block, 0, s, a);
+    parts = sh.ctas;
+    return launch_smem<vq_norm_post_bwd_scalar_kernel<YT, HT>, SCALAR_SMEM>(dim3(sh.ctas), dim3(32 * sh.W * sh.R), sh.smem, s, a);
 }
 
 }  // namespace
 
 size_t norm_workspace_bytes(int H, int T)
 {
-    // at most NORM_PARTS partial rows of each weight, and at most 3 over T (four one-warp rows in a CTA)
-    return (size_t)2 * (size_t)std::min((long)NORM_PARTS, (long)std::max(T, 1) + 3) * (size_t)H * sizeof(float);
+    // at most NORM_PARTS partial rows of each weight, and no more than rows
+    return (size_t)2 * (size_t)std::min(NORM_PARTS, std::max(T, 1)) * (size_t)H * sizeof(float);
 }
 
 cudaError_t launch_norm_pre_bwd(const NormPreBwdArgs &args, int h_dtype, bool vec8, float *dw, float *ws, cudaStream_t s)
