@@ -255,11 +255,10 @@ __device__ __forceinline__ void copy_wait(int pending)
         asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// An ordinary load, so that the compiler may place it (the waits above are its only fences).
 __device__ __forceinline__ uint4 lds128(uint32_t at)
 {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-    return v;
+    return *static_cast<const uint4 *>(__cvta_shared_to_generic(at));
 }
 
 // Pieces of a chunk of 8 elements.

@@ -35,13 +35,13 @@ constexpr uint32_t BF16_ONES = 0x3F803F80u;
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool first)
 {
     if (first)
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
             "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
             : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
     else
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
             "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -64,22 +64,27 @@ __device__ __forceinline__ float2 half_pair(uint32_t v)
     return __half22float2(*reinterpret_cast<const __half2 *>(&v));
 }
 
-// Most warps per CTA (and per row group): the kernels' registers decide.
+// Most warps per CTA (and per row group), and CTAs of that size an SM holds at least: the kernels' registers decide.
 template <int R, int NT>
-constexpr int MAX_WARPS = R == 4 ? 4 : R == 2 && NT < 4 ? 16 : 8;
-constexpr long Q4_WANT_WARPS = 148 * 16;   // 16 warps on every SM
-
-// CTAs of that size an SM holds at least.
+constexpr int MAX_WARPS = R == 4 ? 4 : R == 2 ? 16 : 8;
 template <int R, int NT>
-constexpr int MIN_CTAS = R == 4 ? 4 : NT == 4 || MAX_WARPS<R, NT> == 16 ? 1 : NT == 2 ? 2 : 3;
+constexpr int MIN_CTAS = R == 4 ? 4 : R == 2 ? 1 : NT == 1 ? 3 : 2;
 
-// Bytes of one pipeline stage of a warp: R tiles' words, their scale (and bias)
-// pairs.
+// Bytes of one pipeline stage of a warp: R tiles' words and their scale (and
+// bias) pairs; with x in the ring, 256 more for every live token.
 template <int R, int G, bool BIAS>
 constexpr int STAGE_BYTES = R * (1024 + 32 * (128 / G) * (BIAS ? 2 : 1));
-// Stages per warp: enough bytes in flight per SM with two CTAs resident.
+
+// Whether x goes through the ring too. A warp of four row tiles has enough to
+// do to hide its x loads (from L1, shared with its neighbours); with fewer,
+// each turn would wait for them.
 template <int R>
-constexpr int STAGES = R == 4 ? 2 : R == 2 ? 4 : 6;
+constexpr bool X_RING = R < 4;
+
+// Warps an SM should hold.
+template <int R, int NT>
+constexpr int SM_WARPS = R == 1 && NT == 1 ? 24 : 16;
+constexpr int Q4_SMEM = 222 * 1024;   // shared memory of an SM given to the rings
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
@@ -90,38 +95,45 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
+__device__ __forceinline__ void sts128(uint32_t at, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 template <int NG>
 __device__ __forceinline__ void lds_pairs(uint32_t at, uint32_t (&v)[NG])
 {
+    const void *p = __cvta_shared_to_generic(at);
     if constexpr (NG == 4) {
-        const uint4 t = lds128(at);
+        const uint4 t = *static_cast<const uint4 *>(p);
         v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
     } else if constexpr (NG == 2) {
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at));
+        const uint2 t = *static_cast<const uint2 *>(p);
+        v[0] = t.x, v[1] = t.y;
     } else {
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(at));
+        v[0] = *static_cast<const uint32_t *>(p);
     }
 }
 
 // R: row tiles per warp (of a pair: R / 2 of each module); NT: 8-token tiles.
 // ks of the CTA's warps share a row group of R tiles and take its column tiles
-// in turn.
+// in turn; S stages of SB bytes a warp, S - 1 of them copied ahead.
 template <int R, int NT, int G, bool BIAS>
-__global__ void __launch_bounds__(32 * MAX_WARPS<R, NT>, MIN_CTAS<R, NT>) vq_q4_gemv_kernel(const Q4Args a, int ks)
+__global__ void __launch_bounds__(32 * MAX_WARPS<R, NT>, MIN_CTAS<R, NT>) vq_q4_gemv_kernel(const Q4Args a, int ks, int S, int SB)
 {
     constexpr int NG = 128 / G;           // groups of columns per column tile
     constexpr int SPANS = G / 32;         // 32-column spans per group
-    constexpr int D = STAGES<R>, SB = STAGE_BYTES<R, G, BIAS>, V = R * NT * 4;
-    extern __shared__ __align__(128) unsigned char ring[];   // [warps][D][SB]; later the warps' sums [warps][V][32]
+    constexpr int V = R * NT * 4, XS = STAGE_BYTES<R, G, BIAS>;   // XS: where a stage's x starts
+    extern __shared__ __align__(128) unsigned char ring[];   // [warps][S][SB]; later the warps' sums [warps][V][32]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
-    const int t0 = blockIdx.y * (8 * NT);
+    const int t0 = blockIdx.y * (8 * NT), live = min(8 * NT, a.T - t0);
     const int per = a.pair ? R / 2 : R;   // row tiles of a module per row group
     const int kw = warp & (ks - 1);
     const int grp = blockIdx.x * (blockDim.x / 32 / ks) + warp / ks;
 
     // a lane's place in its row group's tiles; tiles past the last repeat it (their sums are not stored)
-    const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring) + warp * (D * SB);
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring) + warp * (S * SB);
     const uint32_t *wp[R];
     const uint16_t *sp[R], *bp[R];
 #pragma unroll
@@ -149,48 +161,66 @@ __global__ void __launch_bounds__(32 * MAX_WARPS<R, NT>, MIN_CTAS<R, NT>) vq_q4_
                 if constexpr (BIAS)
                     bp[r] += ks * (16 * NG);
             }
+            if constexpr (X_RING<R>) {
+                // 16 chunks of 8 columns a token, odd tokens with their 64-byte halves swapped so that two tokens'
+                // reads meet in no bank; chunks past the last column stay what they were (their scales are 0)
+                for (int i = lane; i < live * 16; i += 32) {
+                    const int n = i >> 4, k = i & 15;
+                    if (sb * 128 + k * 8 < a.cols)
+                        copy_async<16>(at + XS + n * 256 + (k ^ (n & 1) * 4) * 16,
+                                       a.x + (t0 + n) * a.x_ld + sb * 128 + k * 8);
+                }
+            }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        copy_commit();
     };
-    // x fragments of a column tile (of a span for 32 tokens). Tokens past the last read token 0 again (their results
-    // are not stored), spans past the last column its last span (their scales are 0).
+    // x fragments. Tokens past the last read token 0 again (their results are not stored), spans past the last column
+    // something finite: the last span again, or what the ring holds.
     const uint16_t *xp[NT];
+    uint32_t xat[NT], xhalf[NT];   // spans p: xat + 128 (p / 2), + xhalf for even p, + 64 - xhalf for odd p
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-        xp[n] = a.x + (t0 + 8 * n + g < a.T ? (long)(t0 + 8 * n + g) * a.x_ld : 0) + 8 * c;
-    uint4 xv[NT < 4 ? 4 : 1][NT];
+    for (int n = 0; n < NT; ++n) {
+        const int m = 8 * n + g < live ? 8 * n + g : 0;
+        xp[n] = a.x + (t0 + m) * a.x_ld + 8 * c;
+        xat[n] = XS + m * 256 + c * 16;
+        xhalf[n] = (m & 1) * 64;
+    }
+    uint4 xv[X_RING<R> ? 1 : 4][NT];
     auto load_x = [&](int sb, int p, uint4 (&v)[NT]) {
         const int k = min(sb * 128 + p * 32, a.cols - 32);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             v[n] = ldg_u128(xp[n] + k);
     };
-    float acc[R][NT][4];
+    if constexpr (X_RING<R>) {   // chunks that no copy fills hold zeros
+        if (a.cols % 128)
+            for (int i = lane; i < S * (live * 16); i += 32)
+                sts128(base + (i / (live * 16)) * SB + XS + (i % (live * 16)) * 16, make_uint4(0, 0, 0, 0));
+        __syncwarp();
+    }
+    float2 acc[R][NT][2];   // rows g and g + 8, tokens 2 c and 2 c + 1
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[r][n][j] = 0.f;
+            acc[r][n][0] = acc[r][n][1] = splat(0.f);
 
     grid_dep_launch();
     grid_dep_wait();
-#pragma unroll
-    for (int i = 0; i < D - 1; ++i)
+    for (int i = 0; i < S - 1; ++i)
         fetch(kw + i * ks, i);
     int stage = 0;
     for (int sb = kw; sb < a.nsb; sb += ks) {
-        if constexpr (NT < 4) {
+        if constexpr (!X_RING<R>) {
 #pragma unroll
             for (int p = 0; p < 4; ++p)
                 load_x(sb, p, xv[p]);
         }
-        asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory");
-        __syncwarp();   // the stage's scales came through other lanes, and all lanes are done with the stage refilled next
-        fetch(sb + (D - 1) * ks, stage == 0 ? D - 1 : stage - 1);
+        copy_wait(S - 2);
+        __syncwarp();   // scales and x came through other lanes, and all lanes are done with the stage refilled next
+        fetch(sb + (S - 1) * ks, stage == 0 ? S - 1 : stage - 1);
         const uint32_t at = base + stage * SB;
-        stage = stage == D - 1 ? 0 : stage + 1;
+        stage = stage == S - 1 ? 0 : stage + 1;
         uint32_t sc[R][NG], bi[R][NG];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -207,9 +237,12 @@ __global__ void __launch_bounds__(32 * MAX_WARPS<R, NT>, MIN_CTAS<R, NT>) vq_q4_
                 for (int r = 0; r < R; ++r)
                     w[r] = lds128(at + r * 1024 + (p >> 1) * 512 + lane * 16);
             }
-            if constexpr (NT == 4)
-                load_x(sb, p, xv[0]);
-            constexpr int XP = NT < 4 ? 1 : 0;
+            constexpr int XP = X_RING<R> ? 0 : 1;
+            if constexpr (X_RING<R>) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    xv[0][n] = lds128(at + xat[n] + (p >> 1) * 128 + ((p & 1) ? 64 - xhalf[n] : xhalf[n]));
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const bool first = p % SPANS == 0 && h == 0;   // a group's sums start from zero
@@ -235,30 +268,36 @@ __global__ void __launch_bounds__(32 * MAX_WARPS<R, NT>, MIN_CTAS<R, NT>) vq_q4_
                 const int gi = p / SPANS;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
+                    // s sum (q - 8) x + b' sum x with b' = 0 or b + 8 s, as s sum (16 + q) x + (b' - 24 s) sum x
                     const float2 s = half_pair(sc[r][gi]);
-                    float2 b = make_float2(0.f, 0.f);
+                    float2 b = make_float2(-24.f * s.x, -24.f * s.y);
                     if constexpr (BIAS) {
                         b = half_pair(bi[r][gi]);
-                        b = make_float2(fmaf(8.f, s.x, b.x), fmaf(8.f, s.y, b.y));
+                        b = make_float2(fmaf(-16.f, s.x, b.x), fmaf(-16.f, s.y, b.y));
                     }
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float q = fmaf(-24.f, xs[n][j & 1], part[r][n][j]);   // sum (q - 8) x
-                            acc[r][n][j] = fmaf(j < 2 ? s.x : s.y, q, acc[r][n][j]);
-                            if constexpr (BIAS)
-                                acc[r][n][j] = fmaf(j < 2 ? b.x : b.y, xs[n][j & 1], acc[r][n][j]);
-                        }
+                    for (int n = 0; n < NT; ++n) {
+                        const float2 x = make_float2(xs[n][0], xs[n][1]);
+                        acc[r][n][0] = fma2(splat(b.x), x, fma2(splat(s.x), make_float2(part[r][n][0], part[r][n][1]), acc[r][n][0]));
+                        acc[r][n][1] = fma2(splat(b.y), x, fma2(splat(s.y), make_float2(part[r][n][2], part[r][n][3]), acc[r][n][1]));
+                    }
                 }
             }
         }
     }
 
+    float out[R][NT][4];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                out[r][n][j] = (j & 1) ? acc[r][n][j >> 1].y : acc[r][n][j >> 1].x;
     if (ks > 1) {
         float *sums = reinterpret_cast<float *>(ring);
         // every copy has landed (the last turns' groups are empty) and every warp is done with its ring
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        copy_wait(0);
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -266,7 +305,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS<R, NT>, MIN_CTAS<R, NT>) vq_q4_
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    sums[(warp * V + (r * NT + n) * 4 + j) * 32 + lane] = acc[r][n][j];
+                    sums[(warp * V + (r * NT + n) * 4 + j) * 32 + lane] = out[r][n][j];
         __syncthreads();
         // the values are spread over the row group's warps, each adds its own in warp order; of a pair, the warp that
         // stores a value needs both modules' sums
@@ -282,7 +321,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS<R, NT>, MIN_CTAS<R, NT>) vq_q4_
                         float t = 0.f;
                         for (int w = 0; w < ks; ++w)
                             t += s[(w * V + (r * NT + n) * 4 + j) * 32 + lane];
-                        acc[r][n][j] = t;
+                        out[r][n][j] = t;
                     }
                 }
     }
@@ -300,15 +339,15 @@ __global__ void __launch_bounds__(32 * MAX_WARPS<R, NT>, MIN_CTAS<R, NT>) vq_q4_
                 const int token = t0 + 8 * n + 2 * c + (j & 1);
                 if ((v & (ks - 1)) != kw || row >= a.rows || token >= a.T)
                     continue;
-                float out = acc[r][n][j];
+                float o = out[r][n][j];
                 if constexpr (R > 1)
                     if (a.pair)
-                        out = out * sigmoid(out) * acc[r | 1][n][j];
+                        o = o * sigmoid(o) * out[r | 1][n][j];
                 const long yi = (long)token * a.y_ld + row;
                 if (a.y_dtype == VQ_F32)
-                    static_cast<float *>(a.y)[yi] = out;
+                    static_cast<float *>(a.y)[yi] = o;
                 else
-                    static_cast<uint16_t *>(a.y)[yi] = f32_to_bf16_bits(out);
+                    static_cast<uint16_t *>(a.y)[yi] = f32_to_bf16_bits(o);
             }
     }
 }
@@ -357,41 +396,64 @@ __global__ void __launch_bounds__(256) vq_q4_pack_kernel(const uint32_t *codes, 
 }
 
 template <int R, int NT, int G, bool BIAS>
-cudaError_t run(const Q4Args &a, cudaStream_t s)
+cudaError_t run(const Q4Args &a, int ks, cudaStream_t s)
 {
-    const int per = a.pair ? R / 2 : R;
-    const long groups = (a.tiles + per - 1) / per;
-    // warps per row group: enough warps for the GPU, but no more than there are column tiles
-    int ks = 1;
-    while (ks < MAX_WARPS<R, NT> && 2 * ks <= a.nsb && groups * ks < Q4_WANT_WARPS)
-        ks *= 2;
+    const int per = a.pair ? R / 2 : R, groups = (a.tiles + per - 1) / per;
     const int warps = std::max(4, ks);
-    constexpr int PER_WARP = std::max(STAGES<R> * STAGE_BYTES<R, G, BIAS>, R * NT * 4 * 32 * 4);
-    static_assert(MAX_WARPS<R, NT> * PER_WARP <= 227 * 1024);
-    static std::atomic<uint64_t> allowed{0};
-    const cudaError_t e = allow_smem((const void *)vq_q4_gemv_kernel<R, NT, G, BIAS>, MAX_WARPS<R, NT> * PER_WARP, allowed);
-    if (e != cudaSuccess)
-        return e;
-    const dim3 grid((unsigned)((groups + warps / ks - 1) / (warps / ks)), (a.T + 8 * NT - 1) / (8 * NT));
-    return launch_after(vq_q4_gemv_kernel<R, NT, G, BIAS>, grid, dim3(32 * warps), warps * PER_WARP, s, a, ks);
+    const int sb = STAGE_BYTES<R, G, BIAS> + (X_RING<R> ? std::min(a.T, 8 * NT) * 256 : 0);
+    const int stages = R == 4 ? 2 : std::max(2, std::min(4, Q4_SMEM / (std::max(SM_WARPS<R, NT>, warps) * sb)));
+    const size_t smem = (size_t)warps * std::max(stages * sb, R * NT * 4 * 32 * 4);
+    // two stages of the most warps fit
+    static_assert(MAX_WARPS<R, NT> * 2 * (STAGE_BYTES<R, G, BIAS> + (X_RING<R> ? 8 * NT * 256 : 0)) <= Q4_SMEM);
+    const dim3 grid((groups + warps / ks - 1) / (warps / ks), (a.T + 8 * NT - 1) / (8 * NT));
+    return launch_smem<vq_q4_gemv_kernel<R, NT, G, BIAS>, Q4_SMEM>(grid, dim3(32 * warps), smem, s, a, ks, stages, sb);
+}
+
+// The row tiles per warp and the warps per row group with the least estimated
+// time. CTAs run in rounds of what an SM holds; a round takes its warps' turns
+// (a column tile each) and a start and end of about 4 us; a turn takes 0.9 us
+// (1.2 us for 16 tokens), its latency, or its instructions at 4750 per us and
+// SM. Measured over 12 shapes, the choice is within 10% of the best split of
+// each, e.g. (us, R x ks) 6144 x 6144, 1 token: 1 x 8 8.5, 2 x 8 8.9, 4 x 4
+// 12.7; 4096 x 16384, 1 token: 2 x 16 12.6, 1 x 8 20; 131072 x 4096, 8 tokens:
+// 4 x 2 54, 4 x 1 59, 2 x 2 69; 16384 x 4096, 16 tokens: 2 x 4 18, 1 x 8 23.
+// Four row tiles of 16 tokens do not fit the registers.
+struct Q4Split {
+    int R, ks;
+};
+
+Q4Split q4_split(const Q4Args &a, int nt)
+{
+    Q4Split best{1, 1};
+    double least = -1;
+    for (int r = a.pair ? 2 : 1; r <= (nt == 1 ? 4 : 2); r *= 2)
+        for (int k = 1; k <= (r == 4 ? 4 : r == 2 ? 16 : 8) && k <= a.nsb; k *= 2) {
+            const int per = a.pair ? r / 2 : r, w = std::max(4, k);
+            const long groups = (a.tiles + per - 1) / per;
+            const long ctas = (groups + w / k - 1) / (w / k) * ((a.T + 8 * nt - 1) / (8 * nt));
+            const long fits = (r == 1 && nt == 1 ? 24 : 16) / w, on_sm = (ctas + 147) / 148;
+            const double instr = nt == 1 ? 60 + 111 * r : 100 + 175 * r, turns = (a.nsb + k - 1) / k;
+            auto round = [&](long n) {   // n CTAs on an SM
+                return n ? turns * std::max(nt == 1 ? 0.9 : 1.2, n * w * instr / 4750) + 4 : 0.;
+            };
+            const double us = (on_sm / fits) * round(fits) + round(on_sm % fits);
+            if (least < 0 || us < least)
+                least = us, best = {r, k};
+        }
+    return best;
 }
 
 template <int G, bool BIAS>
 cudaError_t pick(const Q4Args &a, cudaStream_t s)
 {
-    const int nt = a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
-    const long tiles = (long)a.tiles * (a.pair ? 2 : 1);
-    // more row tiles per warp once R tiles a group still give every SM its warps (8 per group)
-    const int r = nt < 4 && tiles * 8 >= 4 * Q4_WANT_WARPS ? 4 : a.pair || tiles * 8 >= 2 * Q4_WANT_WARPS ? 2 : 1;
-    switch (r * 8 + nt) {
-    case 9: return run<1, 1, G, BIAS>(a, s);
-    case 10: return run<1, 2, G, BIAS>(a, s);
-    case 12: return run<1, 4, G, BIAS>(a, s);
-    case 17: return run<2, 1, G, BIAS>(a, s);
-    case 18: return run<2, 2, G, BIAS>(a, s);
-    case 20: return run<2, 4, G, BIAS>(a, s);
-    case 33: return run<4, 1, G, BIAS>(a, s);
-    default: return run<4, 2, G, BIAS>(a, s);
+    const int nt = a.T <= 8 ? 1 : 2;
+    const Q4Split q = q4_split(a, nt);
+    switch (q.R * 2 + nt) {
+    case 3: return run<1, 1, G, BIAS>(a, q.ks, s);
+    case 4: return run<1, 2, G, BIAS>(a, q.ks, s);
+    case 5: return run<2, 1, G, BIAS>(a, q.ks, s);
+    case 6: return run<2, 2, G, BIAS>(a, q.ks, s);
+    default: return run<4, 1, G, BIAS>(a, q.ks, s);
     }
 }
 
