@@ -355,9 +355,9 @@ vq_status vq_norm_post(const vq_norm *post, const vq_norm *next, int32_t hidden,
                        const void *h, int32_t h_dtype, int64_t h_ld, float res_scale, float out_scale, int32_t T,
                        void *h_out, int64_t h_out_ld, uint16_t *x_out, int64_t x_out_ld, void *stream);
 
-/* Gradient of vq_norm_post from y, gate and the stored h_out. dh_out: [T, hidden] of h_dtype, or NULL (0): the
- * gradient that reaches h_out past the next norm; dx_out: bf16, required with next, else NULL. With dH = dh_out +
- * (n_next's gradient of dx_out at h_out), s = sigmoid(gate), dv = out_scale * dH:
+/* Gradient of vq_norm_post from y, gate and the stored h_out (needed with next, else may be NULL). dh_out: [T, hidden]
+ * of h_dtype, or NULL (0): the gradient that reaches h_out past the next norm; dx_out: bf16, required with next, else
+ * NULL. With dH = dh_out + (n_next's gradient of dx_out at h_out), s = sigmoid(gate), dv = out_scale * dH:
  *   dh = res_scale * dH                                   (h_dtype; may be dh_out itself, same ld; NULL: not wanted)
  *   dy = n_post's gradient of s * dv at y                 (y_dtype)
  *   dgate = s (1 - s) * dv * u, summed over the row when gate_cols = 1  (gate_dtype; NULL: not wanted)
@@ -384,8 +384,8 @@ size_t vq_balance_workspace_size(int32_t T, int32_t E);
  *   loss      = coef * sum_e (E counts[e] / (V top_k)) probs[e]                       (fp32 [1])
  * (coef when the load is even). A token whose logits are all -Inf has probability 0 everywhere; other Inf and NaN
  * follow IEEE. Masked rows are not read. Column sums run in a fixed order: equal calls give equal bits. Limits as
- * vq_route (E <= 4096, 1 <= top_k <= min(E, 32), T * top_k < 2^31). workspace: 256-byte aligned. T = 0 writes
- * zeros (logits, ids and mask may then be NULL). */
+ * vq_route (E <= 4096, 1 <= top_k <= min(E, 32), T * top_k < 2^31). workspace: 256-byte aligned; calls that may
+ * overlap on the GPU need workspaces of their own. T = 0 writes zeros (logits, ids and mask may then be NULL). */
 vq_status vq_balance_loss(const float *logits, const int32_t *ids, const uint8_t *mask, int32_t T, int32_t E,
                           int32_t top_k, float coef, float *loss, int32_t *counts, float *probs, void *workspace,
                           size_t ws_bytes, void *stream);
@@ -401,8 +401,9 @@ vq_status vq_balance_loss_backward(const float *logits, const int32_t *counts, c
 /* A dense matrix of 4-bit integers with group scales, W [rows, cols]:
  *   W[r, c] = fp32(scale[r, c / group]) * (q[r, c] - 8)                                  without biases
  *   W[r, c] = fp32(scale[r, c / group]) * q[r, c] + fp32(bias[r, c / group])             with biases
- * group is 32, 64 or 128 and divides cols; rows and cols are 1 to 2^30. (The d = 1, 4-bit modules above look their values up in a
- * codebook and have groups of 64 only.) words, scales and biases are in the tile layout that vq_q4_pack writes. */
+ * group is 32, 64 or 128 and divides cols; rows and cols are 1 to 2^30. (The d = 1, 4-bit modules above look their
+ * values up in a codebook and have groups of 64 only.) words, scales and biases are in the tile layout that vq_q4_pack
+ * writes. */
 typedef struct vq_q4_module {
     int32_t rows;
     int32_t cols;
@@ -423,8 +424,7 @@ size_t vq_q4_packed_scales(int32_t rows, int32_t cols, int32_t group);
  * Tile (i, j) (rows 16 i, columns 128 j; j fastest) is 256 words: word ((b * 32) + l) * 4 + s, lane l = 4 g + c,
  * holds rows 16 i + g and 16 i + g + 8, columns k .. k + 3 with k = 128 j + 64 b + 32 (s / 2) + 8 c + 4 (s % 2): rotated
  * right by 4 m bits (m = 0 .. 3), it has the codes of row g + 8 (m % 2), columns k + 2 (m / 2) and k + 2 (m / 2) + 1 in
- * bits 3 to 6 and 19 to 22. A tile's scales
- * are [8 (g)][128 / group][2 (rows g, g + 8)]. */
+ * bits 3 to 6 and 19 to 22. A tile's scales are [8 (g)][128 / group][2 (rows g, g + 8)]. */
 vq_status vq_q4_pack(const uint32_t *codes, const uint16_t *scales, const uint16_t *biases, int32_t rows, int32_t cols,
                      int32_t group, uint32_t *words_out, uint16_t *scales_out, uint16_t *biases_out, void *stream);
 
@@ -436,7 +436,8 @@ vq_status vq_q4_pack(const uint32_t *codes, const uint16_t *scales, const uint16
  * aligned to its element. x enters the tensor cores unrounded as bf16 against the exact integers 16 + q; group sums
  * (24 sum x is taken off them), scales and the sum over groups are fp32 in a fixed order, and y is rounded once: the
  * error is a few 2^-24 of sum |scale| (16 + q) |x|, which has to stay in fp32's range. The weights are streamed once for
- * every 16 tokens: the call is meant for decode-sized T. */
+ * every 16 tokens: the call is meant for decode-sized T (T > 2^20: VQ_ERR_UNSUPPORTED). An Inf or NaN in x gives Inf or
+ * NaN in its token's outputs. */
 vq_status vq_q4_gemv(const vq_q4_module *m0, const vq_q4_module *m1, const uint16_t *x, int64_t x_ld, int32_t T,
                      void *y, int32_t y_dtype, int64_t y_ld, void *stream);
 

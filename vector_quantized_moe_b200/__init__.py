@@ -430,7 +430,7 @@ def norm_pre(norm: Norm, h, out=None, stream=None):
     """x [T, hidden] bf16 = norm(h), the input of a block from the residual stream h (fp32 or bf16) (vq_norm_pre)."""
     if stream is not None:
         return _on_stream(stream, norm_pre, norm, h, out)
-    T, H = len(h), norm.hidden
+    T, H = h.shape[0], norm.hidden
     hp, hd, hl = _row_arg("norm_pre: h", h, T, H)
     if out is None:
         out = _empty(h, _bf16)
@@ -459,7 +459,7 @@ def norm_pre_backward(norm: Norm, h, dx, dres=None, weight_grad: bool = True, wo
     norm, added to dh (vq_norm_pre_backward)."""
     if stream is not None:
         return _on_stream(stream, norm_pre_backward, norm, h, dx, dres, weight_grad, workspace)
-    T, H = len(h), norm.hidden
+    T, H = h.shape[0], norm.hidden
     hp, hd, hl = _row_arg("norm_pre_backward: h", h, T, H)
     xp, _, xl = _row_arg("norm_pre_backward: dx", dx, T, H, VQ_BF16)
     rp, rl = None, 0
@@ -614,7 +614,7 @@ def balance_loss(logits, ids, mask=None, coef: float = 1.0, workspace=None, stre
         return _on_stream(stream, balance_loss, logits, ids, mask, coef, workspace)
     torch = _torch()
     T, E = _logits_arg("balance_loss: logits", logits)
-    if ids.dtype is not torch.int32 or ids.dim() != 2 or len(ids) != T or not ids.is_contiguous():
+    if ids.dtype is not torch.int32 or ids.dim() != 2 or ids.shape[0] != T or not ids.is_contiguous():
         _bad("balance_loss: ids")
     mp = None if mask is None else _mask_arg("balance_loss: mask", mask, T)
     dev = _one_device("balance_loss", logits, ids, mask, workspace)
@@ -696,7 +696,7 @@ def q4_gemv(m: Q4Module, x, up: Optional[Q4Module] = None, out_dtype=None, out=N
     or bfloat16 (the default, or out's)."""
     if stream is not None:
         return _on_stream(stream, q4_gemv, m, x, up, out_dtype, out)
-    T, rows = len(x), m.rows
+    T, rows = x.shape[0], m.rows
     xp, _, xl = _row_arg("q4_gemv: x", x, T, m.cols, VQ_BF16)
     if out is None:
         out = x.new_empty((T, rows), dtype=out_dtype or _bf16)

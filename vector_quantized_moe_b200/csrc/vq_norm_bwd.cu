@@ -618,8 +618,6 @@ __global__ void __launch_bounds__(256) vq_norm_dw_kernel(const float *p1, float 
     grid_dep_wait();
     const float *p = blockIdx.y ? p2 : p1;
     float *d = blockIdx.y ? d2 : d1;
-    if (!d)
-        return;
     const int x = threadIdx.x & 31, yy = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
     float v = 0.f;
     if (c < H) {
@@ -641,7 +639,9 @@ cudaError_t finish(int parts, int H, const float *p1, float *d1, const float *p2
 {
     if (!d1 && !d2)
         return cudaSuccess;
-    return launch_after(vq_norm_dw_kernel, dim3((H + 31) / 32, 2), dim3(256), 0, s, p1, d1, p2, d2, parts, H);
+    if (!d1)
+        p1 = p2, d1 = d2, d2 = nullptr;
+    return launch_after(vq_norm_dw_kernel, dim3((H + 31) / 32, d2 ? 2 : 1), dim3(256), 0, s, p1, d1, p2, d2, parts, H);
 }
 
 constexpr int PRE_BWD_REGS[4] = {64, 88, 112, 128}, POST_BWD_REGS[4] = {96, 128, 128, 128};
