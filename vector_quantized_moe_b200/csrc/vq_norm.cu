@@ -372,7 +372,7 @@ cudaError_t rows(const NormShape &sh, cudaStream_t s, const Args &a)
 template <typename HT>
 cudaError_t pre_launch(NormPreArgs a, bool vec8, cudaStream_t s)
 {
-    const NormShape sh = norm_shape(a.H, a.T, sizeof(HT), 0, PRE_REGS, 256, 0);
+    const NormShape sh = norm_shape(a.H, a.T, sizeof(HT), 0, PRE_REGS, 2, 0);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         switch (sh.nv) {
@@ -391,7 +391,7 @@ template <typename YT, typename HT>
 cudaError_t post_launch(NormPostArgs a, bool vec8, cudaStream_t s)
 {
     const int gate = a.gate_mode != GATE_CHANNEL ? 0 : a.gate_dtype == VQ_F32 ? 4 : 2;
-    const NormShape sh = norm_shape(a.H, a.T, sizeof(YT) + sizeof(HT) + gate, 0, POST_REGS, 256, 0);
+    const NormShape sh = norm_shape(a.H, a.T, sizeof(YT) + sizeof(HT) + gate, 0, POST_REGS, 3, 0);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         switch (sh.nv) {
@@ -422,20 +422,23 @@ NormShape scalar_shape(int H, int T, int floats, int max_ctas)
     return s;
 }
 
-NormShape norm_shape(int H, int T, int bytes, int fixed, const int (&regs)[4], int threads, int max_ctas)
+NormShape norm_shape(int H, int T, int bytes, int fixed, const int (&regs)[4], int max_nv, int max_ctas)
 {
     NormShape s;
     const int chunks = (H + 7) / 8;
-    // rows that stream take fewer threads with more elements each (the row sums and the addresses cost by the warp);
-    // with at most a row or two per SM a row takes as many threads as it can use
-    if (T <= 2 * 148 || chunks > 4 * threads)
-        threads = ROW_THREADS;
-    s.nv = (chunks + threads - 1) / threads;
+    const bool stream = T > 2 * 148;
+    // With at most a row or two per SM a row takes as many threads as it can use. Rows that stream take two chunks a
+    // thread (the row sums and the addresses cost by the warp), more up to the kernel's max_nv before they take over
+    // 256 threads, and share a CTA of 8 warps when they are narrow.
+    s.nv = !stream ? (chunks + ROW_THREADS - 1) / ROW_THREADS
+           : chunks <= 512 ? (chunks <= 32 ? 1 : 2)
+           : chunks <= 256 * max_nv ? (chunks + 255) / 256
+                                    : (chunks + ROW_THREADS - 1) / ROW_THREADS;
     s.W = ((chunks + s.nv - 1) / s.nv + 31) / 32;
-    s.R = s.W == 1 ? 8 : 1;
+    s.R = s.W == 1 || stream ? std::max(1, 8 / s.W) : 1;
     const size_t row = (size_t)32 * s.W * 8 * s.nv, keep = row * fixed, room = NORM_SMEM;
     // with weights in shared memory: rows side by side share them, up to ROW_THREADS threads
-    if (fixed && T > 2 * 148)
+    if (fixed && stream)
         while (2 * s.R * 32 * s.W <= ROW_THREADS && 2 * 2 * s.R * row * bytes + keep <= room)
             s.R *= 2;
     const int block = 32 * s.W * s.R;
