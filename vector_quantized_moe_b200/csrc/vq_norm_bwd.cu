@@ -607,32 +607,30 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
         write_part(a.part2, acc2, reinterpret_cast<float *>(ring), tid, W, a.H);
 }
 
-// Column sums of the partial rows, in row order within each of 8 interleaved
-// strands, then over the strands: d[c] = sum_p part[p][c]. blockIdx.y: which
-// weight gradient.
-__global__ void __launch_bounds__(256) vq_norm_dw_kernel(const float *p1, float *d1, const float *p2, float *d2,
-                                                         int parts, int H)
+// Column sums of the partial rows: 32 columns and 32 interleaved strands of
+// rows per CTA, each strand in row order, then over the strands in order.
+// blockIdx.y: which weight gradient.
+__global__ void __launch_bounds__(1024) vq_norm_dw_kernel(const float *p1, float *d1, const float *p2, float *d2,
+                                                          int parts, int H)
 {
-    __shared__ float s[8][33];
+    __shared__ float s[32][33];
     grid_dep_launch();
     grid_dep_wait();
     const float *p = blockIdx.y ? p2 : p1;
     float *d = blockIdx.y ? d2 : d1;
-    const int x = threadIdx.x & 31, yy = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
+    const int x = threadIdx.x & 31, strand = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
     float v = 0.f;
     if (c < H) {
-#pragma unroll 8
-        for (int i = yy; i < parts; i += 8)
+#pragma unroll 4
+        for (int i = strand; i < parts; i += 32)
             v += p[(long)i * H + c];
     }
-    s[yy][x] = v;
+    s[strand][x] = v;
     __syncthreads();
-    if (yy == 0 && c < H) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i)
-            v += s[i][x];
-        d[c] = v;
-    }
+    // warp w adds the strands of column w
+    v = warp_total(s[x][strand]);
+    if (x == 0 && blockIdx.x * 32 + strand < H)
+        d[blockIdx.x * 32 + strand] = v;
 }
 
 cudaError_t finish(int parts, int H, const float *p1, float *d1, const float *p2, float *d2, cudaStream_t s)
@@ -641,7 +639,7 @@ cudaError_t finish(int parts, int H, const float *p1, float *d1, const float *p2
         return cudaSuccess;
     if (!d1)
         p1 = p2, d1 = d2, d2 = nullptr;
-    return launch_after(vq_norm_dw_kernel, dim3((H + 31) / 32, d2 ? 2 : 1), dim3(256), 0, s, p1, d1, p2, d2, parts, H);
+    return launch_after(vq_norm_dw_kernel, dim3((H + 31) / 32, d2 ? 2 : 1), dim3(1024), 0, s, p1, d1, p2, d2, parts, H);
 }
 
 constexpr int PRE_BWD_REGS[4] = {64, 88, 112, 128}, POST_BWD_REGS[4] = {96, 128, 128, 128};
