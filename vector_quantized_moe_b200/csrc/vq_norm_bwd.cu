@@ -6,7 +6,16 @@
 //
 // Persistent CTAs take rows in turn; a thread keeps its columns' weight
 // gradients in registers over all rows of its CTA, one partial row per CTA goes
-// to the workspace, and a second kernel adds the partial rows in order.
+// to the workspace, and a second kernel adds the partial rows in order. No
+// statistics are saved: the row sums that need only the inputs (|h'|^2, g h',
+// |y|^2) come out of one pass, so recomputing them adds no barrier.
+//
+// Measured: norm_pre's 4096 x 6144 bf16 with a residual gradient 38.2 us for 201 MB
+// (5.3 TB/s, 0.81 of the copy rate); norm_post's 2047 x 4096 with both norms and a
+// gate per channel 48.5 us for 168 MB (3.5 TB/s, 0.53). The second holds 128 registers a
+// thread (two weight gradients), so an SM has 16 warps, at two rows a time; it
+// is bound by their latency between the two row sums (1.8 instructions a
+// cycle), not by HBM.
 #include <algorithm>
 
 #include "vq_block.cuh"
