@@ -170,3 +170,30 @@ def test_repeatable_captured_and_replayed():
     torch.cuda.synchronize()
     got = [o.clone() for o in out]
     assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+def test_two_streams_at_once():
+    T, E, k = 900, 128, 4
+    ins = []
+    for i in range(2):
+        logits = inputs(T, E, k, 20 + i)
+        ins.append((logits, vq.route(logits, k)[0]))
+    want = [vq.balance_loss(*a) for a in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ins]
+    got = [[vq.balance_loss(*a, stream=s) for a, s in zip(ins, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for one in got for p, q in zip(one, want) for a, b in zip(p, q))
+
+
+def test_extreme_logits():
+    # far from zero (the difference to the largest is what counts), and spreads beyond fp32's exponent range
+    T, E, k = 70, 40, 3
+    logits = inputs(T, E, k, 24)
+    logits[:20] += 3.0e4
+    logits[20:40] *= 1.0e4
+    logits[40] = torch.finfo(torch.float32).max
+    logits[41, ::2] = torch.finfo(torch.float32).max
+    logits[41, 1::2] = torch.finfo(torch.float32).min
+    ids = vq.route(logits, k)[0]
+    run_and_check(logits, ids, None, 1.0)

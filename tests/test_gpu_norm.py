@@ -210,3 +210,96 @@ def test_captured_and_replayed_on_new_inputs():
         torch.cuda.synchronize()
         got = [o.clone() for o in out]
         assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+# rows that stream (more than two per SM): every number of chunks a thread and of rows side by side, ragged last CTAs
+STREAM = [(301, 8), (333, 256), (299, 264), (450, 520), (310, 1032), (601, 2056), (300, 4104), (297, 6144), (305, 8200),
+          (298, 16384), (1000, 64), (777, 1024)]
+
+
+@pytest.mark.parametrize("T,H", STREAM)
+@pytest.mark.parametrize("ht,yt,gc,pad", [(BF16, F32, 1, 0), (F32, BF16, -1, 8), (BF16, BF16, 0, 3)])
+def test_streaming_rows(T, H, ht, yt, gc, pad):
+    y, h, dh, dx = (rows(T, H, t, 200 + i, pad) for i, t in enumerate((yt, ht, ht, BF16)))
+    gate = None if gc == 0 else rows(T, 1 if gc == 1 else H, ht, 205, 0, 2.0)
+    n1, n2 = vq.Norm(weight(H, BF16, 206, 0.0), EPS), vq.Norm(weight(H, F32, 207, 1.0), EPS, 1.0)
+    w1, w2 = br.d64(n1.weight), br.d64(n2.weight)
+    br.check("x", vq.norm_pre(n1, h), *br.norm(br.d64(h), w1, 0.0, EPS))
+    (dv, dw), (mv, mw) = br.norm_backward(br.d64(h), w1, 0.0, EPS, br.d64(dx))
+    got, dweight = vq.norm_pre_backward(n1, h, dx, dh)
+    br.check("dh", got, dv + br.d64(dh), mv + br.d64(dh).abs())
+    br.check("dweight", dweight, dw, mw)
+    ho, x = vq.norm_post(y, h, n1, gate, 0.5, 2.0, n2)
+    v, m = br.branch(br.d64(y), w1, 0.0, EPS, br.d64(gate), 2.0)
+    br.check("h_out", ho, 0.5 * br.d64(h) + v, 0.5 * br.d64(h).abs() + m)
+    br.check("x_out", x, *br.norm(br.d64(ho), w2, 1.0, EPS))
+    # the definition takes one offset for both norms: the next norm's is folded into its weight
+    got = vq.norm_post_backward(y, ho, dh, dx, n1, gate, 0.5, 2.0, n2)
+    ref, mag = br.post_backward(br.d64(y), br.d64(ho), br.d64(dh), br.d64(dx), w1, w2 + 1.0, 0.0, EPS, br.d64(gate), 0.5,
+                                2.0)
+    for name, g, r, m in zip(("dy", "dgate", "dh", "dpost", "dnext"), got, ref, mag):
+        if r is not None:
+            br.check(name, g, r, m)
+
+
+def _stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+@pytest.mark.parametrize("T,H", [(5, 512), (700, 512), (40, 257)])
+def test_gradients_in_place(T, H):
+    # the C calls allow dh on top of the residual gradient it adds
+    n1, n2 = vq.Norm(weight(H, BF16, 220, 0.0)), vq.Norm(weight(H, BF16, 221, 0.0))
+    h, dx, y = rows(T, H, BF16, 222), rows(T, H, BF16, 223), rows(T, H, F32, 224)
+    grad = rows(T, H, BF16, 225)
+    want, _ = vq.norm_pre_backward(n1, h, dx, grad, weight_grad=False)
+    buf = grad.clone()
+    st = vq._L().vq_norm_pre_backward(n1._ref, h.data_ptr(), vq.VQ_BF16, H, dx.data_ptr(), H, buf.data_ptr(), H, T,
+                                      buf.data_ptr(), H, None, None, 0, _stream())
+    assert st == 0 and torch.equal(buf, want)
+    dy, _, dh, _, _ = vq.norm_post_backward(y, h, grad, dx, n1, None, 0.5, 1.0, n2)
+    buf, dy2 = grad.clone(), torch.empty_like(y)
+    st = vq._L().vq_norm_post_backward(n1._ref, n2._ref, H, y.data_ptr(), vq.VQ_F32, H, None, 0, 0, 0, h.data_ptr(),
+                                       vq.VQ_BF16, H, 0.5, 1.0, T, buf.data_ptr(), H, dx.data_ptr(), H, dy2.data_ptr(), H,
+                                       None, 0, buf.data_ptr(), H, None, None, None, 0, _stream())
+    assert st == 0 and torch.equal(buf, dh) and torch.equal(dy2, dy)
+
+
+def test_two_streams_at_once():
+    T, H = 600, 1024
+    n = vq.Norm(weight(H, BF16, 230, 0.0))
+    ins = [(rows(T, H, BF16, 231 + i), rows(T, H, BF16, 235 + i)) for i in range(2)]
+    want = [vq.norm_pre_backward(n, h, dx) for h, dx in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ins]
+    got = [[vq.norm_pre_backward(n, h, dx, stream=s) for (h, dx), s in zip(ins, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for one in got for p, q in zip(one, want) for a, b in zip(p, q))
+
+
+def test_rows_far_apart():
+    # rows 2^30 elements apart: offsets beyond 32 bits
+    H = 512
+    far = lambda: torch.zeros(2 * 2 ** 30 + H, dtype=BF16, device="cuda").as_strided((3, H), (2 ** 30, 1))  # noqa: E731
+    h, x = far(), far()
+    h.copy_(rows(3, H, BF16, 240))
+    n = vq.Norm(weight(H, BF16, 241, 0.0))
+    vq.norm_pre(n, h, out=x)
+    br.check("x", x, *br.norm(br.d64(h), br.d64(n.weight), 0.0, EPS))
+    dh, _ = vq.norm_pre_backward(n, h, x, h)
+    (dv, _), (mv, _) = br.norm_backward(br.d64(h), br.d64(n.weight), 0.0, EPS, br.d64(x))
+    br.check("dh", dh, dv + br.d64(h), mv + br.d64(h).abs())
+
+
+def test_first_call_may_be_captured():
+    # a width and types that nothing here has launched before: the launch's own set-up happens inside the capture
+    T, H = 320, 12288
+    y, h = rows(T, H, BF16, 250), rows(T, H, F32, 251)
+    n1, n2 = vq.Norm(weight(H, F32, 252, 0.0)), vq.Norm(weight(H, F32, 253, 0.0))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = vq.norm_post(y, h, n1, next=n2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, vq.norm_post(y, h, n1, next=n2)))

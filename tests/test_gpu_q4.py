@@ -172,3 +172,47 @@ def test_empty_batch_streams_and_replay():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, vq.q4_gemv(m, x))
+
+
+# shapes whose estimate picks each split: row tiles per warp x warps per row group, for one and for two token tiles
+SPLITS = [(70000, 128, 64, False), (70016, 320, 32, True), (40000, 160, 32, False), (20000, 512, 128, True),
+          (9600, 512, 64, False), (5000, 1024, 128, True), (40, 4096, 32, True)]
+
+
+@pytest.mark.parametrize("rows,cols,group,biased", SPLITS)
+@pytest.mark.parametrize("T", [3, 13])
+def test_every_split(rows, cols, group, biased, T):
+    raw, m = module(rows, cols, group, biased, rows)
+    x = tokens(T, cols, 20)
+    ref, mag = br.q4(*raw, group, br.d64(x))
+    br.check("y", vq.q4_gemv(m, x, out_dtype=F32), ref, mag)
+
+
+@pytest.mark.parametrize("rows,cols,T", [(40000, 128, 2), (20000, 160, 8), (9600, 512, 5), (9600, 512, 11), (100, 2048, 2)])
+def test_every_split_of_a_pair(rows, cols, T):
+    r0, m0 = module(rows, cols, 32, True, 21)
+    r1, m1 = module(rows, cols, 32, True, 22)
+    x = tokens(T, cols, 23)
+    ref, mag = br.q4_pair(*br.q4(*r0, 32, br.d64(x)), *br.q4(*r1, 32, br.d64(x)))
+    br.check("y", vq.q4_gemv(m0, x, m1, F32), ref, mag)
+
+
+def test_two_streams_at_once():
+    raw, m = module(3000, 1024, 64, True, 24)
+    xs = [tokens(4, 1024, 25 + i) for i in range(2)]
+    want = [vq.q4_gemv(m, x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[vq.q4_gemv(m, x, stream=s) for x, s in zip(xs, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for pair in got for g, w in zip(pair, want))
+
+
+def test_rows_of_q4_far_apart():
+    # token and output rows 2^30 elements apart: offsets beyond 32 bits
+    raw, m = module(64, 256, 64, False, 27)
+    x = torch.zeros(2 * 2 ** 30 + 256, dtype=BF16, device="cuda").as_strided((3, 256), (2 ** 30, 1))
+    y = torch.zeros(2 * 2 ** 30 + 64, dtype=BF16, device="cuda").as_strided((3, 64), (2 ** 30, 1))
+    x.copy_(tokens(3, 256, 28))
+    vq.q4_gemv(m, x, out=y)
+    br.check("y", y, *br.q4(*raw, 64, br.d64(x)))
