@@ -377,7 +377,7 @@ cudaError_t rows(const NormShape &sh, cudaStream_t s, const Args &a)
 template <typename HT>
 cudaError_t pre_launch(NormPreArgs a, bool vec8, cudaStream_t s)
 {
-    const NormShape sh = norm_shape(a.H, a.T, sizeof(HT), 0, PRE_REGS, 2, 0);
+    const NormShape sh = norm_shape(a.H, a.T, sizeof(HT), 0, PRE_REGS, 2, 2, 0);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         switch (sh.nv) {
@@ -396,7 +396,7 @@ template <typename YT, typename HT>
 cudaError_t post_launch(NormPostArgs a, bool vec8, cudaStream_t s)
 {
     const int gate = a.gate_mode != GATE_CHANNEL ? 0 : a.gate_dtype == VQ_F32 ? 4 : 2;
-    const NormShape sh = norm_shape(a.H, a.T, sizeof(YT) + sizeof(HT) + gate, 0, POST_REGS, 3, 0);
+    const NormShape sh = norm_shape(a.H, a.T, sizeof(YT) + sizeof(HT) + gate, 0, POST_REGS, 2, 3, 0);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         switch (sh.nv) {
@@ -427,16 +427,18 @@ NormShape scalar_shape(int H, int T, int floats, int max_ctas)
     return s;
 }
 
-NormShape norm_shape(int H, int T, int bytes, int fixed, const int (&regs)[4], int max_nv, int max_ctas)
+NormShape norm_shape(int H, int T, int bytes, int fixed, const int (&regs)[4], int nv, int max_nv,
+                     int max_ctas)
 {
     NormShape s;
     const int chunks = (H + 7) / 8;
     const bool stream = T > 2 * 148;
-    // With at most a row or two per SM a row takes as many threads as it can use. Rows that stream take two chunks a
-    // thread (the row sums and the addresses cost by the warp), more up to the kernel's max_nv before they take over
-    // 256 threads, and share a CTA of 8 warps when they are narrow.
+    // With at most a row or two per SM a row takes as many threads as it can use. Rows that stream take the kernel's nv
+    // chunks a thread (the row sums and the addresses cost by the warp), more up to its max_nv before they take over
+    // 256 threads, and share a CTA of 8 warps when they are narrow. Measured (us) with 1, 2, 3 and 4 chunks: post 4096 x
+    // 4096 29.1, 27.8, 28.3, 33.6; pre backward 38.5, 31.1, 31.3, 27.3; post backward 100, 81, 134, 105.
     s.nv = !stream ? (chunks + ROW_THREADS - 1) / ROW_THREADS
-           : chunks <= 512 ? (chunks <= 32 ? 1 : 2)
+           : chunks <= 512 ? std::min(nv, (chunks + 31) / 32)
            : chunks <= 256 * max_nv ? (chunks + 255) / 256
                                     : (chunks + ROW_THREADS - 1) / ROW_THREADS;
     s.W = ((chunks + s.nv - 1) / s.nv + 31) / 32;

@@ -113,9 +113,9 @@ struct NormShape {
 constexpr int ROW_THREADS = 512;           // most threads a row
 constexpr int NORM_SMEM = 222 * 1024;      // shared memory of an SM given to the rings
 // bytes: of input an element copied ahead; fixed: bytes an element kept for the whole launch; regs: registers a
-// thread at nv chunks (regs[nv - 1]); max_nv: the most chunks a thread has registers for when rows stream; max_ctas:
-// 0, or the most CTAs.
-NormShape norm_shape(int H, int T, int bytes, int fixed, const int (&regs)[4], int max_nv, int max_ctas);
+// thread at nv chunks (regs[nv - 1]); nv, max_nv: chunks a thread takes when rows stream, and the most it has
+// registers for; max_ctas: 0, or the most CTAs.
+NormShape norm_shape(int H, int T, int bytes, int fixed, const int (&regs)[4], int nv, int max_nv, int max_ctas);
 
 // The same for the element-by-element kernels: about 256 threads a CTA, `floats` fp32 values an element in shared
 // memory for each of its rows side by side.

@@ -663,7 +663,7 @@ cudaError_t rows(const NormShape &sh, cudaStream_t s, const Args &a)
 template <typename HT>
 cudaError_t pre_bwd(NormPreBwdArgs a, bool vec8, int &parts, cudaStream_t s)
 {
-    NormShape sh = norm_shape(a.H, a.T, sizeof(HT) * (a.dres ? 2 : 1) + 2, 0, PRE_BWD_REGS, 4, NORM_PARTS);
+    NormShape sh = norm_shape(a.H, a.T, sizeof(HT) * (a.dres ? 2 : 1) + 2, 0, PRE_BWD_REGS, 4, 4, NORM_PARTS);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         parts = sh.ctas;
@@ -686,7 +686,7 @@ cudaError_t post_bwd(NormPostBwdArgs a, bool vec8, int &parts, cudaStream_t s)
     const int gate = a.gate_mode != GATE_CHANNEL ? 0 : a.gate_dtype == VQ_F32 ? 4 : 2;
     auto w = [](const NormDev &n) { return !n.weight ? 0 : n.dtype == VQ_F32 ? 4 : 2; };
     NormShape sh = norm_shape(a.H, a.T, sizeof(YT) + (a.dho ? sizeof(HT) : 0) + (a.next.weight ? sizeof(HT) + 2 : 0) + gate,
-                              w(a.post) + w(a.next), POST_BWD_REGS, 2, NORM_PARTS);
+                              w(a.post) + w(a.next), POST_BWD_REGS, 2, 2, NORM_PARTS);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         parts = sh.ctas;

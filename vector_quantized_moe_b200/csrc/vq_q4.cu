@@ -143,16 +143,20 @@ __global__ void __launch_bounds__(32 * MAX_WARPS<R, NT>, MIN_CTAS<R, NT>) vq_q4_
 
     // a lane's place in its row group's tiles; tiles past the last repeat it (their sums are not stored)
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring) + warp * (S * SB);
+    auto tile_at = [&](int r) {
+        return min((long)grp * per + (a.pair ? r >> 1 : r), (long)a.tiles - 1) * a.nsb + kw;
+    };
     const uint32_t *wp[R];
-    const uint16_t *sp[R], *bp[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const bool up = a.pair && (r & 1);
-        const long at = min((long)grp * per + (a.pair ? r >> 1 : r), (long)a.tiles - 1) * a.nsb + kw;
-        wp[r] = (up ? a.words[1] : a.words[0]) + at * 256 + lane * 4;
-        sp[r] = (up ? a.scales[1] : a.scales[0]) + (at * 8 + g) * (2 * NG);
-        bp[r] = BIAS ? (up ? a.biases[1] : a.biases[0]) + (at * 8 + g) * (2 * NG) : nullptr;
-    }
+    for (int r = 0; r < R; ++r)
+        wp[r] = (a.pair && (r & 1) ? a.words[1] : a.words[0]) + tile_at(r) * 256 + lane * 4;
+    // scales: the lanes of column c copy tile c's, the next R columns its biases (a second copy where R is 4)
+    const int cr = c & (R - 1);
+    const bool cup = a.pair && (cr & 1), scale_lane = c < R, bias_lane = BIAS && R < 4 && c >= R && c < 2 * R;
+    const long scale_at = (tile_at(cr) * 8 + g) * (2 * NG);
+    const uint16_t *sp = (bias_lane ? (cup ? a.biases[1] : a.biases[0]) : (cup ? a.scales[1] : a.scales[0])) + scale_at;
+    const uint16_t *bp = BIAS && R == 4 ? (cup ? a.biases[1] : a.biases[0]) + scale_at : nullptr;
+    const uint32_t sdst = R * 1024 + (((bias_lane ? R : 0) + cr) * 8 + g) * (4 * NG);
     auto fetch = [&](int sb, int stage) {
         if (sb < a.nsb) {
             const uint32_t at = base + stage * SB;
@@ -161,14 +165,13 @@ __global__ void __launch_bounds__(32 * MAX_WARPS<R, NT>, MIN_CTAS<R, NT>) vq_q4_
                 copy_async<16>(at + r * 1024 + lane * 16, wp[r]);
                 copy_async<16>(at + r * 1024 + 512 + lane * 16, wp[r] + 128);
                 wp[r] += ks * 256;
-                if (c == 0) {
-                    copy_async<4 * NG>(at + R * 1024 + (r * 8 + g) * (4 * NG), sp[r]);
-                    if constexpr (BIAS)
-                        copy_async<4 * NG>(at + R * 1024 + ((R + r) * 8 + g) * (4 * NG), bp[r]);
-                }
-                sp[r] += ks * (16 * NG);
-                if constexpr (BIAS)
-                    bp[r] += ks * (16 * NG);
+            }
+            if (scale_lane || bias_lane)
+                copy_async<4 * NG>(at + sdst, sp);
+            sp += ks * (16 * NG);
+            if constexpr (BIAS && R == 4) {
+                copy_async<4 * NG>(at + sdst + R * 8 * (4 * NG), bp);
+                bp += ks * (16 * NG);
             }
             if constexpr (X_RING<R>) {
                 // 16 chunks of 8 columns a token, odd tokens with their 64-byte halves swapped so that two tokens'
