@@ -62,30 +62,10 @@ cudaError_t launch_smem(dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args
 // Two fp32 operations per instruction (fma.rn.f32x2 and its kin): the row
 // kernels are bound by instruction issue before they are by HBM.
 
-__device__ __forceinline__ uint64_t bits2(float2 v) { return *reinterpret_cast<const uint64_t *>(&v); }
-__device__ __forceinline__ float2 pair2(uint64_t v) { return *reinterpret_cast<const float2 *>(&v); }
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
-
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-    return pair2(d);
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
-    return pair2(d);
-}
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
-    return pair2(d);
-}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 
 // ---------------------------------------------------------------- chunks of a row
 //

@@ -48,13 +48,27 @@ __device__ __forceinline__ float weight_at(const void *p, int dtype, long i)
     return dtype == VQ_F32 ? static_cast<const float *>(p)[i] : element(static_cast<const uint16_t *>(p)[i]);
 }
 
-// The fast exponential and reciprocal: their error is a few 2^-24 times max(1, |z|), that of a rounding of z.
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 2^x and 1 / x of the special function unit (ex2.approx, rcp.approx: a few 2^-24 off; results below 2^-126 are 0).
+__device__ __forceinline__ float ex2_ftz(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_ftz(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
-// sigmoid(z) and sigmoid(-z) from one exponential and one division by a number in [1, 2].
+// sigmoid(z), off by a few 2^-24 times max(1, |z|), as a rounding of z is.
+__device__ __forceinline__ float sigmoid(float z) { return rcp_ftz(1.f + ex2_ftz(-1.4426950408889634f * z)); }
+
+// sigmoid(z) and sigmoid(-z) from one exponential and one reciprocal of a number in [1, 2].
 __device__ __forceinline__ void sigmoids(float z, float &on, float &off)
 {
-    const float e = __expf(-fabsf(z)), s = __fdividef(1.f, 1.f + e), r = e * s;
+    const float e = ex2_ftz(-1.4426950408889634f * fabsf(z)), s = rcp_ftz(1.f + e), r = e * s;
     on = z < 0.f ? r : s;
     off = z < 0.f ? s : r;
 }
