@@ -329,7 +329,8 @@ typedef struct vq_norm {
 vq_status vq_norm_pre(const vq_norm *n, const void *h, int32_t h_dtype, int64_t h_ld, int32_t T, uint16_t *x,
                       int64_t x_ld, void *stream);
 
-/* Bytes of workspace the two norm backward calls need for T rows of `hidden`; 0 on invalid sizes. */
+/* Bytes of workspace the two norm backward calls need for T rows of `hidden`: 0 up to 4 rows (workspace may be NULL),
+ * and on invalid sizes. */
 size_t vq_norm_workspace_size(int32_t hidden, int32_t T);
 
 /* Gradient of vq_norm_pre. dx: bf16 [T, hidden]; dres: NULL, or [T, hidden] of h_dtype, a gradient that reaches h
@@ -337,8 +338,8 @@ size_t vq_norm_workspace_size(int32_t hidden, int32_t T);
  *   dh = r g - r^3 h mean(g h) + dres        (h_dtype; may be dres itself, same ld)
  *   dweight = sum_t dx h r                   (fp32 [hidden], or NULL: not computed)
  * The sum over rows runs in a fixed order: equal calls give equal bits. T = 0 writes dweight = 0. workspace:
- * 256-byte aligned, vq_norm_workspace_size bytes; needed (VQ_ERR_WORKSPACE) only with dweight. Calls that may
- * overlap on the GPU need workspaces of their own. */
+ * 256-byte aligned, vq_norm_workspace_size bytes; needed (VQ_ERR_WORKSPACE) only with dweight and more than 4 rows.
+ * Calls that may overlap on the GPU need workspaces of their own. */
 vq_status vq_norm_pre_backward(const vq_norm *n, const void *h, int32_t h_dtype, int64_t h_ld, const uint16_t *dx,
                                int64_t dx_ld, const void *dres, int64_t dres_ld, int32_t T, void *dh, int64_t dh_ld,
                                float *dweight, void *workspace, size_t ws_bytes, void *stream);

@@ -35,10 +35,10 @@ def test_norm_pre(kw, status):
 def test_norm_workspace_size():
     f = vq._L().vq_norm_workspace_size
     assert f(0, 4) == 0 and f(16385, 4) == 0 and f(64, -1) == 0
-    assert 0 < f(64, 1) < f(64, 100) <= f(64, 1 << 30)
+    assert f(64, 4) == 0 < f(64, 5) < f(64, 100) <= f(64, 1 << 30)
 
 
-def pre_bwd(n=None, h=8192, hl=64, dx=16384, dxl=64, dres=None, dresl=0, T=4, dh=32768, dhl=64, dw=65536, ws=1 << 20,
+def pre_bwd(n=None, h=8192, hl=64, dx=16384, dxl=64, dres=None, dresl=0, T=8, dh=32768, dhl=64, dw=65536, ws=1 << 20,
             nws=1 << 30):
     n = norm() if n is None else n
     return vq._L().vq_norm_pre_backward(ctypes.byref(n), h, 1, hl, dx, dxl, dres, dresl, T, dh, dhl, dw, ws, nws, None)
@@ -72,7 +72,7 @@ def test_norm_post(kw, status):
     assert post(**kw) == status
 
 
-def post_bwd(p=None, n=None, y=8192, gate=None, gc=1, ho=16384, T=4, dho=32768, dholl=64, dx=None, dy=65536, dyl=64,
+def post_bwd(p=None, n=None, y=8192, gate=None, gc=1, ho=16384, T=8, dho=32768, dholl=64, dx=None, dy=65536, dyl=64,
              dgate=None, dh=131072, dp=None, dn=None, ws=1 << 20, nws=1 << 30, hd=1):
     r = lambda v: None if v is None else ctypes.byref(v)  # noqa: E731
     return vq._L().vq_norm_post_backward(r(p), r(n), 64, y, 0, 64, gate, 1, gc, gc, ho, hd, 64, 1.0, 1.0, T, dho, dholl,

@@ -303,3 +303,32 @@ def test_first_call_may_be_captured():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, vq.norm_post(y, h, n1, next=n2)))
+
+
+@pytest.mark.parametrize("T", [1, 2, 4, 5, 300])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_weight_gradients_of_few_rows_and_off_16_bytes(T, offset):
+    H = 640
+    n1, n2 = vq.Norm(weight(H, BF16, 260, 0.0), EPS), vq.Norm(weight(H, F32, 261, 0.0), EPS)
+    h, dx, y = rows(T, H, BF16, 262), rows(T, H, BF16, 263), rows(T, H, F32, 264)
+    ws = torch.empty(vq._norm_ws(H, T) + 256, dtype=torch.uint8, device="cuda")
+    wp = (ws.data_ptr() + 255) // 256 * 256
+    buf = torch.full((2, H + 8), float("nan"), device="cuda")
+    d1, d2 = (b[offset:offset + H] for b in buf)
+    dh, dy = torch.empty_like(h), torch.empty_like(y)
+    st = vq._L().vq_norm_pre_backward(n1._ref, h.data_ptr(), vq.VQ_BF16, H, dx.data_ptr(), H, None, 0, T, dh.data_ptr(), H,
+                                      d1.data_ptr(), wp, ws.numel() - 256, _stream())
+    assert st == 0
+    (dv, dw), (mv, mw) = br.norm_backward(br.d64(h), br.d64(n1.weight), 0.0, EPS, br.d64(dx))
+    br.check("dh", dh, dv, mv)
+    br.check("dweight", d1, dw, mw)
+    st = vq._L().vq_norm_post_backward(n1._ref, n2._ref, H, y.data_ptr(), vq.VQ_F32, H, None, 0, 0, 0, h.data_ptr(),
+                                       vq.VQ_BF16, H, 1.0, 1.0, T, None, 0, dx.data_ptr(), H, dy.data_ptr(), H, None, 0,
+                                       None, 0, d1.data_ptr(), d2.data_ptr(), wp, ws.numel() - 256, _stream())
+    assert st == 0
+    ref, mag = br.post_backward(br.d64(y), br.d64(h), None, br.d64(dx), br.d64(n1.weight), br.d64(n2.weight), 0.0, EPS,
+                                None, 1.0, 1.0)
+    br.check("dy", dy, ref[0], mag[0])
+    br.check("dpost", d1, ref[3], mag[3])
+    br.check("dnext", d2, ref[4], mag[4])
+    assert bool(torch.isnan(buf[:, offset + H:]).all()) and bool(torch.isnan(buf[:, :offset]).all())

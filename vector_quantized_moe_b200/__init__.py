@@ -449,7 +449,7 @@ def _empty(like, dtype):
     return like.new_empty(like.shape, dtype=dtype)
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=1024)
 def _norm_ws(H, T):
     return int(_L().vq_norm_workspace_size(H, T))
 
@@ -470,9 +470,11 @@ def norm_pre_backward(norm: Norm, h, dx, dres=None, weight_grad: bool = True, wo
     dw = wp = dp = None
     nb = 0
     if weight_grad:
-        dw = h.new_empty(H, dtype=_f32)
+        dw = _empty(norm.weight, _f32)
         dp = dw.data_ptr()
-        workspace, wp, nb = _workspace(_norm_ws(H, T), workspace, h)
+        nb = _norm_ws(H, T)
+        if nb:
+            workspace, wp, nb = _workspace(nb, workspace, h)
     _launch("vq_norm_pre_backward", dev, norm._ref, hp, hd, hl, xp, xl, rp, rl, T, dh.data_ptr(), H, dp, wp, nb)
     return dh, dw
 
@@ -573,13 +575,15 @@ def norm_post_backward(y, h_out, dh_out, dx_out=None, post: Optional[Norm] = Non
         dgate = gate.new_empty(gate.shape, dtype=_f32 if gd == VQ_F32 else _bf16)
         zp = dgate.data_ptr()
     if post is not None:
-        dpost = y.new_empty(H, dtype=_f32)
+        dpost = _empty(w1, _f32)
         d1 = dpost.data_ptr()
     if next is not None:
-        dnext = y.new_empty(H, dtype=_f32)
+        dnext = _empty(w2, _f32)
         d2 = dnext.data_ptr()
     if post is not None or next is not None:
-        workspace, wp, nb = _workspace(_norm_ws(H, T), workspace, y)
+        nb = _norm_ws(H, T)
+        if nb:
+            workspace, wp, nb = _workspace(nb, workspace, y)
     _launch("vq_norm_post_backward", dev, pr, nr, H, yp, yd, yl, gp, gd, gc, gl, hp, hd, hl, res_scale, out_scale, T, ap,
             al, xp, xl, dy.data_ptr(), H, zp, gc, dh.data_ptr(), H, d1, d2, wp, nb)
     return dy, dgate, dh, dpost, dnext
@@ -601,7 +605,7 @@ def _logits_arg(where, logits):
     return logits.shape
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=1024)
 def _balance_ws(T, E):
     return int(_L().vq_balance_workspace_size(T, E))
 
@@ -699,11 +703,17 @@ def q4_gemv(m: Q4Module, x, up: Optional[Q4Module] = None, out_dtype=None, out=N
     T, rows = x.shape[0], m.rows
     xp, _, xl = _row_arg("q4_gemv: x", x, T, m.cols, VQ_BF16)
     if out is None:
+        yd = VQ_BF16 if out_dtype is None else _codes.get(out_dtype)
+        if yd is None:
+            _bad("q4_gemv: out_dtype")
+        dev = _one_device("q4_gemv", x, m.words, None if up is None else up.words)
         out = x.new_empty((T, rows), dtype=out_dtype or _bf16)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        _bad("q4_gemv: out_dtype")
-    yp, yd, yl = _row_arg("q4_gemv: out", out, T, rows)
-    dev = _one_device("q4_gemv", x, m.words, out, None if up is None else up.words)
+        yp, yl = out.data_ptr(), rows
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            _bad("q4_gemv: out_dtype")
+        yp, yd, yl = _row_arg("q4_gemv: out", out, T, rows)
+        dev = _one_device("q4_gemv", x, m.words, out, None if up is None else up.words)
     _launch("vq_q4_gemv", dev, m._ref, None if up is None else up._ref, xp, xl, T, yp, yd, yl)
     return out
 

@@ -58,6 +58,11 @@ struct Rows {
         if (n && !aligned(n->weight, 16))
             vec8 = false;
     }
+    void gradient(const float *d)   // a weight's: a few rows' kernels write it themselves
+    {
+        if (!aligned(d, 16))
+            vec8 = false;
+    }
 };
 
 vq_status check_hidden(int32_t hidden, int32_t T)
@@ -69,7 +74,7 @@ vq_status check_hidden(int32_t hidden, int32_t T)
 
 vq_status check_ws(const void *ws, size_t bytes, size_t need)
 {
-    return ws && aligned(ws, 256) && bytes >= need ? VQ_OK : VQ_ERR_WORKSPACE;
+    return need == 0 || (ws && aligned(ws, 256) && bytes >= need) ? VQ_OK : VQ_ERR_WORKSPACE;
 }
 
 bool balance_sizes_ok(int32_t T, int32_t E, int32_t k)
@@ -153,6 +158,7 @@ vq_status vq_norm_pre_backward(const vq_norm *n, const void *h, int32_t h_dtype,
         return r.st;
     if (!aligned(dweight, 4))
         return VQ_ERR_ALIGN;
+    r.gradient(dweight);
     if (dweight && (st = check_ws(workspace, ws_bytes, norm_workspace_bytes(n->hidden, T))) != VQ_OK)
         return st;
     NormPreBwdArgs a{};
@@ -272,6 +278,8 @@ vq_status vq_norm_post_backward(const vq_norm *post, const vq_norm *next, int32_
         return r.st;
     if (!aligned(dpost, 4) || !aligned(dnext, 4))
         return VQ_ERR_ALIGN;
+    r.gradient(dpost);
+    r.gradient(dnext);
     if ((dpost || dnext) && (st = check_ws(workspace, ws_bytes, norm_workspace_bytes(hidden, T))) != VQ_OK)
         return st;
     NormPostBwdArgs a{};
@@ -319,7 +327,7 @@ vq_status vq_balance_loss(const float *logits, const int32_t *ids, const uint8_t
     if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(probs, 4))
         return VQ_ERR_ALIGN;
     const size_t need = balance_workspace_bytes(T, E);
-    const vq_status st = need ? check_ws(workspace, ws_bytes, need) : VQ_OK;
+    const vq_status st = check_ws(workspace, ws_bytes, need);
     if (st != VQ_OK)
         return st;
     BalanceArgs a{};

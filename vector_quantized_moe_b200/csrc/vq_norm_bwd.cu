@@ -25,6 +25,7 @@ namespace vq {
 namespace {
 
 constexpr int NORM_PARTS = 592;     // most partial rows: 4 CTAs on each of 148 SMs
+constexpr int NORM_ONE_CTA = 4;     // up to so many rows one CTA takes them all and writes the weight gradients itself
 
 template <int VEC>
 __device__ __forceinline__ int chunk_at(int i, int tid, int W) { return (tid + i * 32 * W) * VEC; }
@@ -663,7 +664,8 @@ cudaError_t rows(const NormShape &sh, cudaStream_t s, const Args &a)
 template <typename HT>
 cudaError_t pre_bwd(NormPreBwdArgs a, bool vec8, int &parts, cudaStream_t s)
 {
-    NormShape sh = norm_shape(a.H, a.T, sizeof(HT) * (a.dres ? 2 : 1) + 2, 0, PRE_BWD_REGS, 4, 4, NORM_PARTS);
+    const int most = a.part && a.T <= NORM_ONE_CTA ? 1 : NORM_PARTS;
+    NormShape sh = norm_shape(a.H, a.T, sizeof(HT) * (a.dres ? 2 : 1) + 2, 0, PRE_BWD_REGS, 4, 4, most);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         parts = sh.ctas;
@@ -674,7 +676,7 @@ cudaError_t pre_bwd(NormPreBwdArgs a, bool vec8, int &parts, cudaStream_t s)
         default: return rows<vq_norm_pre_bwd_kernel<HT, 4>>(sh, s, a);
         }
     }
-    sh = scalar_shape(a.H, a.T, 1, NORM_PARTS);
+    sh = scalar_shape(a.H, a.T, 1, most);
     a.W = sh.W;
     parts = sh.ctas;
     return launch_smem<vq_norm_pre_bwd_scalar_kernel<HT>, SCALAR_SMEM>(dim3(sh.ctas), dim3(32 * sh.W * sh.R), sh.smem, s, a);
@@ -685,8 +687,9 @@ cudaError_t post_bwd(NormPostBwdArgs a, bool vec8, int &parts, cudaStream_t s)
 {
     const int gate = a.gate_mode != GATE_CHANNEL ? 0 : a.gate_dtype == VQ_F32 ? 4 : 2;
     auto w = [](const NormDev &n) { return !n.weight ? 0 : n.dtype == VQ_F32 ? 4 : 2; };
+    const int most = (a.part1 || a.part2) && a.T <= NORM_ONE_CTA ? 1 : NORM_PARTS;
     NormShape sh = norm_shape(a.H, a.T, sizeof(YT) + (a.dho ? sizeof(HT) : 0) + (a.next.weight ? sizeof(HT) + 2 : 0) + gate,
-                              w(a.post) + w(a.next), POST_BWD_REGS, 2, 2, NORM_PARTS);
+                              w(a.post) + w(a.next), POST_BWD_REGS, 2, 2, most);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         parts = sh.ctas;
@@ -697,7 +700,7 @@ cudaError_t post_bwd(NormPostBwdArgs a, bool vec8, int &parts, cudaStream_t s)
         default: return rows<vq_norm_post_bwd_kernel<YT, HT, 4>>(sh, s, a);
         }
     }
-    sh = scalar_shape(a.H, a.T, 3, NORM_PARTS);
+    sh = scalar_shape(a.H, a.T, 3, most);
     a.W = sh.W;
     parts = sh.ctas;
     return launch_smem<vq_norm_post_bwd_scalar_kernel<YT, HT>, SCALAR_SMEM>(dim3(sh.ctas), dim3(32 * sh.W * sh.R), sh.smem, s, a);
@@ -707,30 +710,34 @@ cudaError_t post_bwd(NormPostBwdArgs a, bool vec8, int &parts, cudaStream_t s)
 
 size_t norm_workspace_bytes(int H, int T)
 {
+    if (T <= NORM_ONE_CTA)
+        return 0;
     // at most NORM_PARTS partial rows of each weight, and no more than rows
-    return (size_t)2 * (size_t)std::min(NORM_PARTS, std::max(T, 1)) * (size_t)H * sizeof(float);
+    return (size_t)2 * (size_t)std::min(NORM_PARTS, T) * (size_t)H * sizeof(float);
 }
 
 cudaError_t launch_norm_pre_bwd(const NormPreBwdArgs &args, int h_dtype, bool vec8, float *dw, float *ws, cudaStream_t s)
 {
     NormPreBwdArgs a = args;
-    a.part = dw ? ws : nullptr;
+    const bool one = a.T > 0 && a.T <= NORM_ONE_CTA;
+    a.part = !dw ? nullptr : one ? dw : ws;
     int parts = 0;
     if (a.T > 0) {
         const cudaError_t e = h_dtype == VQ_F32 ? pre_bwd<float>(a, vec8, parts, s) : pre_bwd<uint16_t>(a, vec8, parts, s);
         if (e != cudaSuccess)
             return e;
     }
-    return finish(parts, a.H, a.part, dw, nullptr, nullptr, s);
+    return one ? cudaSuccess : finish(parts, a.H, a.part, dw, nullptr, nullptr, s);
 }
 
 cudaError_t launch_norm_post_bwd(const NormPostBwdArgs &args, int y_dtype, int h_dtype, bool vec8, float *dpost,
                                  float *dnext, float *ws, cudaStream_t s)
 {
     NormPostBwdArgs a = args;
+    const bool one = a.T > 0 && a.T <= NORM_ONE_CTA;
     // the second half of the workspace holds dnext's partial rows
-    a.part1 = dpost ? ws : nullptr;
-    a.part2 = dnext ? ws + norm_workspace_bytes(a.H, a.T) / (2 * sizeof(float)) : nullptr;
+    a.part1 = !dpost ? nullptr : one ? dpost : ws;
+    a.part2 = !dnext ? nullptr : one ? dnext : ws + norm_workspace_bytes(a.H, a.T) / (2 * sizeof(float));
     int parts = 0;
     if (a.T > 0) {
         cudaError_t e;
@@ -742,7 +749,7 @@ cudaError_t launch_norm_post_bwd(const NormPostBwdArgs &args, int y_dtype, int h
         if (e != cudaSuccess)
             return e;
     }
-    return finish(parts, a.H, a.part1, dpost, a.part2, dnext, s);
+    return one ? cudaSuccess : finish(parts, a.H, a.part1, dpost, a.part2, dnext, s);
 }
 
 }  // namespace vq
