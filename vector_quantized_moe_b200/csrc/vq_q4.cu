@@ -21,11 +21,11 @@
 // fragments serve R tiles; the CTA's warps take column tiles in turn and add
 // their sums through shared memory in warp order.
 //
-// Measured (GPU time): 131072 x 4096, 8 tokens 54.5 us for 281 MB (5.2 TB/s, 0.79 of the
+// Measured (GPU time): 131072 x 4096, 8 tokens 53.3 us for 281 MB (5.3 TB/s, 0.81 of the
 // copy rate; the copies alone, without decoding and mma, take 45 us); bound by
 // the ALU pipe (65% busy: three shifts and four mask-ors per word, 7 per 8
-// weights, at half rate) and the latency of 16 warps on an SM. 6144 x 6144, 1 token 8.5
-// us for 21 MB, 2 x 2040 x 6144, 16 tokens 8.9 us: 3 to 6 turns of a warp at 0.9 to 1.2 us and
+// weights, at half rate) and the latency of 16 warps on an SM. 6144 x 6144, 1 token 8.3
+// us for 21 MB, 2 x 2040 x 6144, 16 tokens 8.7 us: 3 to 6 turns of a warp at 0.9 to 1.2 us and
 // 2 to 4 us of start and end. The subtraction of 8 as an instruction: 171
 // instructions a 16 x 128 tile instead of 126. Shifts as high multiplies on
 // the FMA pipe: 73 us. Persistent CTAs that copy ahead across row groups: 64 us.
