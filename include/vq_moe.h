@@ -329,7 +329,7 @@ typedef struct vq_norm {
 vq_status vq_norm_pre(const vq_norm *n, const void *h, int32_t h_dtype, int64_t h_ld, int32_t T, uint16_t *x,
                       int64_t x_ld, void *stream);
 
-/* Bytes of workspace the two norm backward calls need for T rows of `hidden`: 0 up to 4 rows (workspace may be NULL),
+/* Bytes of workspace the two norm backward calls need for T rows of `hidden`: 0 for one row (workspace may be NULL),
  * and on invalid sizes. */
 size_t vq_norm_workspace_size(int32_t hidden, int32_t T);
 
@@ -338,7 +338,7 @@ size_t vq_norm_workspace_size(int32_t hidden, int32_t T);
  *   dh = r g - r^3 h mean(g h) + dres        (h_dtype; may be dres itself, same ld)
  *   dweight = sum_t dx h r                   (fp32 [hidden], or NULL: not computed)
  * The sum over rows runs in a fixed order: equal calls give equal bits. T = 0 writes dweight = 0. workspace:
- * 256-byte aligned, vq_norm_workspace_size bytes; needed (VQ_ERR_WORKSPACE) only with dweight and more than 4 rows.
+ * 256-byte aligned, vq_norm_workspace_size bytes; needed (VQ_ERR_WORKSPACE) only with dweight and more than one row.
  * Calls that may overlap on the GPU need workspaces of their own. */
 vq_status vq_norm_pre_backward(const vq_norm *n, const void *h, int32_t h_dtype, int64_t h_ld, const uint16_t *dx,
                                int64_t dx_ld, const void *dres, int64_t dres_ld, int32_t T, void *dh, int64_t dh_ld,

@@ -305,10 +305,10 @@ def test_first_call_may_be_captured():
     assert all(torch.equal(a, b) for a, b in zip(out, vq.norm_post(y, h, n1, next=n2)))
 
 
-@pytest.mark.parametrize("T", [1, 2, 4, 5, 300])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 17, 300])
+@pytest.mark.parametrize("H", [40, 640, 6144])
 @pytest.mark.parametrize("offset", [0, 1])
-def test_weight_gradients_of_few_rows_and_off_16_bytes(T, offset):
-    H = 640
+def test_weight_gradients_of_few_rows_and_off_16_bytes(T, H, offset):
     n1, n2 = vq.Norm(weight(H, BF16, 260, 0.0), EPS), vq.Norm(weight(H, F32, 261, 0.0), EPS)
     h, dx, y = rows(T, H, BF16, 262), rows(T, H, BF16, 263), rows(T, H, F32, 264)
     ws = torch.empty(vq._norm_ws(H, T) + 256, dtype=torch.uint8, device="cuda")

@@ -58,7 +58,7 @@ struct Rows {
         if (n && !aligned(n->weight, 16))
             vec8 = false;
     }
-    void gradient(const float *d)   // a weight's: a few rows' kernels write it themselves
+    void gradient(const float *d)   // a weight's: one row's kernel writes it itself
     {
         if (!aligned(d, 16))
             vec8 = false;

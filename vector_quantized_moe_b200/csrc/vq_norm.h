@@ -141,7 +141,7 @@ cudaError_t launch_norm_pre(const NormPreArgs &a, int h_dtype, bool vec8, cudaSt
 cudaError_t launch_norm_post(const NormPostArgs &a, int y_dtype, int h_dtype, bool vec8, cudaStream_t s);
 
 // The backward launches sum the weight gradients over the rows in `ws`
-// (norm_workspace_bytes; none for a few rows) and finish them in d1 / d2 (each may be NULL).
+// (norm_workspace_bytes; none for one row) and finish them in d1 / d2 (each may be NULL).
 size_t norm_workspace_bytes(int H, int T);
 cudaError_t launch_norm_pre_bwd(const NormPreBwdArgs &a, int h_dtype, bool vec8, float *dw, float *ws, cudaStream_t s);
 cudaError_t launch_norm_post_bwd(const NormPostBwdArgs &a, int y_dtype, int h_dtype, bool vec8, float *dpost,

@@ -25,7 +25,6 @@ namespace vq {
 namespace {
 
 constexpr int NORM_PARTS = 592;     // most partial rows: 4 CTAs on each of 148 SMs
-constexpr int NORM_ONE_CTA = 4;     // up to so many rows one CTA takes them all and writes the weight gradients itself
 
 template <int VEC>
 __device__ __forceinline__ int chunk_at(int i, int tid, int W) { return (tid + i * 32 * W) * VEC; }
@@ -664,8 +663,7 @@ cudaError_t rows(const NormShape &sh, cudaStream_t s, const Args &a)
 template <typename HT>
 cudaError_t pre_bwd(NormPreBwdArgs a, bool vec8, int &parts, cudaStream_t s)
 {
-    const int most = a.part && a.T <= NORM_ONE_CTA ? 1 : NORM_PARTS;
-    NormShape sh = norm_shape(a.H, a.T, sizeof(HT) * (a.dres ? 2 : 1) + 2, 0, PRE_BWD_REGS, 4, 4, most);
+    NormShape sh = norm_shape(a.H, a.T, sizeof(HT) * (a.dres ? 2 : 1) + 2, 0, PRE_BWD_REGS, 4, 4, NORM_PARTS);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         parts = sh.ctas;
@@ -676,7 +674,7 @@ cudaError_t pre_bwd(NormPreBwdArgs a, bool vec8, int &parts, cudaStream_t s)
         default: return rows<vq_norm_pre_bwd_kernel<HT, 4>>(sh, s, a);
         }
     }
-    sh = scalar_shape(a.H, a.T, 1, most);
+    sh = scalar_shape(a.H, a.T, 1, NORM_PARTS);
     a.W = sh.W;
     parts = sh.ctas;
     return launch_smem<vq_norm_pre_bwd_scalar_kernel<HT>, SCALAR_SMEM>(dim3(sh.ctas), dim3(32 * sh.W * sh.R), sh.smem, s, a);
@@ -687,9 +685,8 @@ cudaError_t post_bwd(NormPostBwdArgs a, bool vec8, int &parts, cudaStream_t s)
 {
     const int gate = a.gate_mode != GATE_CHANNEL ? 0 : a.gate_dtype == VQ_F32 ? 4 : 2;
     auto w = [](const NormDev &n) { return !n.weight ? 0 : n.dtype == VQ_F32 ? 4 : 2; };
-    const int most = (a.part1 || a.part2) && a.T <= NORM_ONE_CTA ? 1 : NORM_PARTS;
     NormShape sh = norm_shape(a.H, a.T, sizeof(YT) + (a.dho ? sizeof(HT) : 0) + (a.next.weight ? sizeof(HT) + 2 : 0) + gate,
-                              w(a.post) + w(a.next), POST_BWD_REGS, 2, 2, most);
+                              w(a.post) + w(a.next), POST_BWD_REGS, 2, 2, NORM_PARTS);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         parts = sh.ctas;
@@ -700,7 +697,7 @@ cudaError_t post_bwd(NormPostBwdArgs a, bool vec8, int &parts, cudaStream_t s)
         default: return rows<vq_norm_post_bwd_kernel<YT, HT, 4>>(sh, s, a);
         }
     }
-    sh = scalar_shape(a.H, a.T, 3, most);
+    sh = scalar_shape(a.H, a.T, 3, NORM_PARTS);
     a.W = sh.W;
     parts = sh.ctas;
     return launch_smem<vq_norm_post_bwd_scalar_kernel<YT, HT>, SCALAR_SMEM>(dim3(sh.ctas), dim3(32 * sh.W * sh.R), sh.smem, s, a);
@@ -710,7 +707,10 @@ cudaError_t post_bwd(NormPostBwdArgs a, bool vec8, int &parts, cudaStream_t s)
 
 size_t norm_workspace_bytes(int H, int T)
 {
-    if (T <= NORM_ONE_CTA)
+    // One row's CTA writes the weight gradients itself. For more rows the second launch (about 1 us) costs less than rows
+    // in turn in one CTA (norm_post, 6144 wide, 2 and 4 rows: 11.2 and 19.7 us against 9.6) or the partial rows added
+    // through the shared memory of a cluster of 8 (4, 16, 32 rows: 10.6, 13.9, 22.6 us against 9.7, 9.8, 10.0).
+    if (T <= 1)
         return 0;
     // at most NORM_PARTS partial rows of each weight, and no more than rows
     return (size_t)2 * (size_t)std::min(NORM_PARTS, T) * (size_t)H * sizeof(float);
@@ -719,7 +719,7 @@ size_t norm_workspace_bytes(int H, int T)
 cudaError_t launch_norm_pre_bwd(const NormPreBwdArgs &args, int h_dtype, bool vec8, float *dw, float *ws, cudaStream_t s)
 {
     NormPreBwdArgs a = args;
-    const bool one = a.T > 0 && a.T <= NORM_ONE_CTA;
+    const bool one = a.T == 1;
     a.part = !dw ? nullptr : one ? dw : ws;
     int parts = 0;
     if (a.T > 0) {
@@ -734,7 +734,7 @@ cudaError_t launch_norm_post_bwd(const NormPostBwdArgs &args, int y_dtype, int h
                                  float *dnext, float *ws, cudaStream_t s)
 {
     NormPostBwdArgs a = args;
-    const bool one = a.T > 0 && a.T <= NORM_ONE_CTA;
+    const bool one = a.T == 1;
     // the second half of the workspace holds dnext's partial rows
     a.part1 = !dpost ? nullptr : one ? dpost : ws;
     a.part2 = !dnext ? nullptr : one ? dnext : ws + norm_workspace_bytes(a.H, a.T) / (2 * sizeof(float));
