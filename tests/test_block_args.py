@@ -201,3 +201,13 @@ def test_binding_refuses_wrong_tensors():
     refused(vq.q4_gemv, m, t(2, 64))
     refused(vq.q4_gemv, m, t(2, 64), out_dtype=torch.float32, out=t(2, 64))
     refused(vq.q4_gemv, m, t(2, 64), out=t(2, 60))
+
+
+def test_workspaces_too_small_or_scattered():
+    like = t(1)
+    room = t(1024, dtype=torch.uint8)
+    for first in range(0, 257, 16):   # fewer bytes than to the next 256-byte boundary: none are usable, never less
+        _, at, n = vq._workspace(64, room[first:first + 8], like)
+        assert at % 256 == 0 and 0 <= n <= 8
+    refused(vq._workspace, 64, room[:1].expand(1 << 20), like)
+    refused(vq._workspace, 64, room[::2], like)

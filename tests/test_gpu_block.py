@@ -1,5 +1,7 @@
 """The block operators together: norm -> router -> experts and 4-bit shared expert -> gate -> norm, residual, next norm,
 then the router's balance loss, as a decode step and as a prompt, against the oracle's experts and the definitions."""
+import types
+
 import numpy as np
 import pytest
 import torch
@@ -104,3 +106,88 @@ def test_hidden_sizes_are_checked():
     block, _, _ = make(False, False, False)
     with pytest.raises(vq.VQError):
         vq.MoEBlock(block.layer, vq.Norm(torch.ones(H + 8, device="cuda")), block.router, K)
+
+
+def test_small_workspace_is_refused():
+    n = vq.Norm(torch.ones(H, device="cuda"))
+    h = stream(8, 40, torch.bfloat16)
+    room = torch.empty(4096, dtype=torch.uint8, device="cuda")
+    for ws in (room[128:130], room[:0], room[:1].expand(1 << 20)):
+        with pytest.raises(vq.VQError):
+            vq.norm_pre_backward(n, h, h, workspace=ws)
+
+
+def test_stream_of_another_device_is_refused():
+    h = stream(2, 41)
+    with pytest.raises(vq.VQError):
+        vq.norm_pre(vq.Norm(torch.ones(H, device="cuda")), h, stream=types.SimpleNamespace(device_index=1))
+
+
+def test_weights_outlive_a_call_on_another_stream():
+    # a weight given up right after the call may not be handed out again before the call has run
+    h, s, last = stream(4096, 42), torch.cuda.Stream(), torch.cuda.Event()
+    want = vq.norm_pre(vq.Norm(torch.full((H,), 2.0, device="cuda")), h)
+    torch.cuda.synchronize()
+    w = torch.full((H,), 2.0, device="cuda")
+    n = vq.Norm(w)
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            torch.mm(h, h.T)   # work ahead of the call on its stream
+    got = vq.norm_pre(n, h, stream=s)
+    last.record(s)
+    del n, w
+    others = [torch.full((H,), 3.0, device="cuda") for _ in range(64)]
+    last.synchronize()
+    assert torch.equal(got, want) and len(others) == 64
+
+
+def test_router_and_x_are_checked():
+    block, _, _ = make(False, False, False)
+    h = stream(3, 43)
+    x = vq.norm_pre(block.pre, h)
+    router = block.router
+    for wrong in (lambda v: router(v).to(torch.bfloat16), lambda v: router(v)[:, :4], lambda v: router(v)[:2],
+                  lambda v: router(v).T.contiguous().T, lambda v: router(v).cpu()):
+        block.router = wrong
+        with pytest.raises(vq.VQError):
+            block.decode(h)
+    block.router = router
+    for wrong in (x[:2], x.float(), torch.zeros(3, 2 * H, dtype=torch.bfloat16, device="cuda")[:, :H]):
+        with pytest.raises(vq.VQError):
+            block.decode(h, wrong)
+    assert torch.equal(block.decode(h)[0], block.decode(h, x)[0])
+
+
+def test_two_graphs_and_a_larger_batch_share_nothing():
+    # two captured steps replayed at once on two streams, after eager calls of other sizes have grown and gone
+    block, _, _ = make(True, True, True)
+    hs = [stream(2, 50, torch.bfloat16), stream(5, 51, torch.bfloat16)]
+    want = [block.decode(h) for h in hs]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for h in hs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(block.decode(h))
+        graphs.append(g)
+    block.decode(stream(16, 52, torch.bfloat16))
+    junk = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    streams = [torch.cuda.Stream() for _ in hs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert len(junk) == 8
+    for got, w in zip(outs, want):
+        assert all(torch.equal(p, q) for p, q in zip(got, w))
+
+
+def test_given_workspace_holds_the_error_word():
+    block, _, _ = make(True, True, True)
+    h = stream(4, 60, torch.bfloat16)
+    ws = torch.empty(block.layer.workspace_size(4, K, vq.VQ_MODE_DECODE) + 256, dtype=torch.uint8, device="cuda")
+    assert all(torch.equal(p, q) for p, q in zip(block.decode(h, workspace=ws), block.decode(h)))
+    assert vq.fit_check(ws) == 0

@@ -358,13 +358,19 @@ def _bad(where: str):
 
 
 def _on_stream(stream, f, *args):
-    """f(*args) with `stream` current: its outputs are allocated on it, its inputs are held until it has run."""
+    """f(*args) with `stream` current: its outputs are allocated on it, its inputs (those of norms and modules too) are
+    held until it has run."""
     torch = _torch()
+    held = []
+    for a in args:
+        held += a._held() if isinstance(a, (Norm, Q4Module)) else [a]
+    held = [t for t in held if isinstance(t, torch.Tensor) and t.is_cuda]
+    if any(t.get_device() != stream.device_index for t in held):
+        _bad(f.__name__ + " (stream of another device)")
     with torch.cuda.stream(stream):
         out = f(*args)
-    for t in args:
-        if isinstance(t, torch.Tensor) and t.is_cuda:
-            t.record_stream(stream)
+    for t in held:
+        t.record_stream(stream)
     return out
 
 
@@ -405,9 +411,11 @@ def _one_device(where, first, *others) -> int:
 def _workspace(n, given, like):
     """(tensor, aligned pointer, bytes) of a workspace of n bytes: the given one, or a new one on like's device."""
     ws = given if given is not None else like.new_empty(n + 256, dtype=_torch().uint8)
+    if not ws.is_contiguous():
+        _bad("workspace")
     base = ws.data_ptr()
     aligned = (base + 255) // 256 * 256
-    return ws, aligned, ws.numel() * ws.element_size() - (aligned - base)
+    return ws, aligned, max(0, ws.numel() * ws.element_size() - (aligned - base))
 
 
 class Norm:
@@ -424,6 +432,9 @@ class Norm:
         self.weight, self.hidden = weight, weight.numel()
         self._s = vq_norm(self.hidden, code, weight.data_ptr(), eps, offset)
         self._ref = ctypes.byref(self._s)
+
+    def _held(self):
+        return [self.weight]
 
 
 def norm_pre(norm: Norm, h, out=None, stream=None):
@@ -664,6 +675,9 @@ class Q4Module:
         self._s = vq_q4_module(rows, cols, group, _ptr(words), _ptr(scales), _ptr(biases))
         self._ref = ctypes.byref(self._s)
 
+    def _held(self):
+        return [self.words, self.scales, self.biases]
+
     @classmethod
     def from_rows(cls, words, scales, biases=None, group: int = 64, stream=None):
         """Lays row-major device arrays out (vq_q4_pack): words int32 [rows, cols / 8] (pack(codes, 4)'s rows), scales
@@ -827,7 +841,9 @@ class MoEBlock:
         h' = res_scale * h + out_scale * post(y),   x' = next(h')
 
     router: x [T, hidden] bf16 -> logits fp32 [T, E]. shared: (gate, up, down) Q4Modules of a SwiGLU expert that every
-    token takes; shared_gate: x -> logits [T, 1], None for 1. post and next may be None."""
+    token takes; shared_gate: x -> logits [T, 1], None for 1. post and next may be None. Every call has an experts'
+    workspace of its own, so calls on several streams, or captured into several graphs, do not meet in one; a given
+    `workspace` (256 bytes more than layer.workspace_size) can be asked for its error word (fit_check)."""
 
     def __init__(self, layer: MoELayer, pre: Norm, router, top_k: int, post: Optional[Norm] = None,
                  next: Optional[Norm] = None, shared=None, shared_gate=None, renorm: bool = True,
@@ -838,19 +854,34 @@ class MoEBlock:
         self.router, self.shared, self.shared_gate = router, shared, shared_gate
         self.top_k, self.renorm, self.res_scale, self.out_scale = top_k, renorm, res_scale, out_scale
 
-    def decode(self, h, x=None):
+    def decode(self, h, x=None, workspace=None):
         """(h', x', router logits) for decode-sized batches; x' is None without `next`."""
-        return self._run(self.layer.decode, h, x)
+        return self._run(self.layer.decode, VQ_MODE_DECODE, h, x, workspace)
 
-    def prefill(self, h, x=None):
+    def prefill(self, h, x=None, workspace=None):
         """The same for prefill-sized batches."""
-        return self._run(self.layer.prefill, h, x)
+        return self._run(self.layer.prefill, VQ_MODE_PREFILL, h, x, workspace)
 
-    def _run(self, experts, h, x):
+    def _run(self, experts, mode, h, x, workspace):
+        dev = _one_device("MoEBlock", h, x, workspace)
+        if dev != _device():
+            with _torch().cuda.device(dev):
+                return self._run(experts, mode, h, x, workspace)
         if x is None:
             x = norm_pre(self.pre, h)
+        elif x.dtype is not _bf16 or x.shape != h.shape or not x.is_contiguous():
+            _bad("MoEBlock: x")
+        T = x.shape[0]
         logits = self.router(x)
-        y = experts(x, logits, self.top_k, self.renorm, out_dtype=_f32)
+        if logits.dtype is not _f32 or logits.shape != (T, self.layer.E) or not logits.is_contiguous():
+            _bad("MoEBlock: router logits")
+        _one_device("MoEBlock: router logits", x, logits)
+        if workspace is None:
+            n = self.layer.workspace_size(T, self.top_k, mode)
+            if n == 0:
+                _bad("MoEBlock: tokens or top_k")
+            workspace = x.new_empty(n + 256, dtype=_torch().uint8)
+        y = experts(x, logits, self.top_k, self.renorm, out_dtype=_f32, workspace=workspace)
         if self.shared is not None:
             gate, up, down = self.shared
             s = q4_gemv(down, q4_gemv(gate, x, up))
