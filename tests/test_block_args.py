@@ -131,6 +131,7 @@ def q4m(rows=64, cols=128, group=64, words=4096, scales=8192, biases=None):
     (dict(m=q4m(scales=None)), ARG), (dict(m=q4m(words=4100)), ALIGN), (dict(m=q4m(biases=8200)), ALIGN),
     (dict(up=q4m(rows=32)), ARG), (dict(up=q4m(group=128)), ARG), (dict(up=q4m(biases=8192)), ARG),
     (dict(x=None), ARG), (dict(y=None), ARG), (dict(T=-1), ARG), (dict(T=(1 << 20) + 1), UNSUPPORTED), (dict(yd=4), ARG),
+    (dict(T=16 * 65535 + 1), UNSUPPORTED),
     (dict(xl=64), ARG), (dict(yl=8), ARG), (dict(x=16392), ALIGN), (dict(xl=132), ALIGN), (dict(y=32770, yd=0), ALIGN),
     (dict(y=32769), ALIGN), (dict(T=0, x=None, y=None), 0),
 ])

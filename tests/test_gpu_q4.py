@@ -216,3 +216,28 @@ def test_rows_of_q4_far_apart():
     x.copy_(tokens(3, 256, 28))
     vq.q4_gemv(m, x, out=y)
     br.check("y", y, *br.q4(*raw, 64, br.d64(x)))
+
+
+def test_most_tokens():
+    T = 16 * 65535
+    raw, m = module(3, 32, 32, True, 30)
+    x = tokens(T, 32, 31)
+    ref, mag = br.q4(*raw, 32, br.d64(x))
+    br.check("y", vq.q4_gemv(m, x, out_dtype=F32), ref, mag)
+
+
+@pytest.mark.parametrize("rows", [70000, 40000, 512])
+def test_x_rewritten_by_the_call_before(rows):
+    # each product reads the x that the launch before it wrote over the one that the product before that read
+    raw, m = module(rows, 128, 64, False, 32)
+    n = vq.Norm(torch.ones(128, device="cuda"))
+    hs = [torch.randn((8, 128), generator=torch.Generator().manual_seed(33 + i)).cuda() for i in range(20)]
+    xs = [vq.norm_pre(n, h) for h in hs]
+    want = [vq.q4_gemv(m, x) for x in xs]
+    x, got = torch.empty_like(xs[0]), []
+    torch.cuda.synchronize()
+    for h in hs:
+        vq.norm_pre(n, h, out=x)
+        got.append(vq.q4_gemv(m, x))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -82,7 +82,7 @@ bool balance_sizes_ok(int32_t T, int32_t E, int32_t k)
     return T >= 0 && E >= 1 && E <= 4096 && k >= 1 && k <= std::min(E, 32) && (long)T * k < (1L << 31);
 }
 
-constexpr int32_t Q4_MAX_COLS = 1 << 30, Q4_MAX_T = 1 << 20;
+constexpr int32_t Q4_MAX_COLS = 1 << 30, Q4_MAX_T = 16 * 65535;   // 16 tokens to a CTA, grid.y
 
 bool q4_sizes_ok(int32_t rows, int32_t cols, int32_t group)
 {
