@@ -1,0 +1,99 @@
+"""What the block operators' binding hands to the library, and what it refuses before it does: weights and modules as
+they are at the call. CPU tensors throughout; the library's launch is replaced by a record of its arguments."""
+import ctypes
+
+import pytest
+import torch
+
+import vector_quantized_moe_b200 as vq
+
+BF16, F32 = torch.bfloat16, torch.float32
+ARG, WORKSPACE = 1, 4
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    """The launches that a call would make, as (name, args); every tensor passes for one on GPU 0."""
+    made = []
+    vq.Norm(torch.ones(8))   # binds the library and torch's types
+    monkeypatch.setattr(vq, "_one_device", lambda where, first, *others: 0)
+    monkeypatch.setattr(vq, "_launch", lambda name, dev, *args: made.append((name, args)))
+    return made
+
+
+def struct(ref):
+    """A copy of the struct behind a byref() as it is now."""
+    return type(ref._obj).from_buffer_copy(ref._obj)
+
+
+def address(t):
+    return t.data_ptr()
+
+
+CALLS = {
+    "norm_pre": lambda n, v: vq.norm_pre(n, v),
+    "norm_pre_backward": lambda n, v: vq.norm_pre_backward(n, v, v),
+    "norm_post, post": lambda n, v: vq.norm_post(v, v, n),
+    "norm_post, next": lambda n, v: vq.norm_post(v, v, next=n),
+    "norm_post_backward, post": lambda n, v: vq.norm_post_backward(v, v, v, post=n),
+    "norm_post_backward, next": lambda n, v: vq.norm_post_backward(v, v, v, v, next=n),
+}
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_norm_uses_the_weight_it_has_at_the_call(launches, call):
+    def weight_of():
+        launches.clear()
+        CALLS[call](n, v)
+        ref = launches[0][1][1 if call.endswith("next") else 0]
+        return struct(ref)
+
+    v = torch.zeros((2, 64), dtype=BF16)
+    w = torch.nn.Parameter(torch.ones(64))
+    n = vq.Norm(w, 1e-5, 1.0)
+    first = w.data
+    assert weight_of().weight == address(w)
+    w.data = torch.full((64,), 2.0)                      # new data of the same parameter
+    got = weight_of()
+    assert got.weight == address(w) != address(first) and got.weight_dtype == vq.VQ_F32
+    n.weight = torch.full((64,), 3.0, dtype=BF16)        # another weight, of another type
+    got = weight_of()
+    assert got.weight == address(n.weight) and got.weight_dtype == vq.VQ_BF16
+    assert (got.hidden, got.weight_offset) == (64, 1.0) and abs(got.eps - 1e-5) < 1e-12
+    n.weight = torch.ones(32)                            # of another width: the rows no longer fit
+    with pytest.raises(vq.VQError):
+        weight_of()
+    n.weight = torch.ones(64, dtype=torch.float16)       # of a type that no norm takes
+    with pytest.raises(vq.VQError):
+        weight_of()
+
+
+def q4_arrays(rows, cols, group, biased=False):
+    words = torch.zeros(vq._L().vq_q4_packed_words(rows, cols), dtype=torch.int32)
+    scales = torch.zeros(vq._L().vq_q4_packed_scales(rows, cols, group), dtype=torch.int16)
+    return words, scales, scales.clone() if biased else None
+
+
+@pytest.mark.parametrize("pair", [False, True])
+def test_a_4_bit_module_uses_the_arrays_it_has_at_the_call(launches, pair):
+    def structs():
+        launches.clear()
+        vq.q4_gemv(m, x, up)
+        return [struct(r) for r in launches[0][1][:2] if r is not None]
+
+    x = torch.zeros((2, 128), dtype=BF16)
+    m = vq.Q4Module(64, 128, 64, *q4_arrays(64, 128, 64, True))
+    up = vq.Q4Module(64, 128, 64, *q4_arrays(64, 128, 64, True)) if pair else None
+    last = up if pair else m
+    assert structs()[-1].words == address(last.words)
+    old = last.words.data
+    last.words.data = last.words.clone()
+    assert structs()[-1].words == address(last.words) != address(old)
+    for name in ("scales", "biases"):
+        setattr(last, name, getattr(last, name).clone())
+        assert getattr(structs()[-1], name) == address(getattr(last, name))
+    s = structs()[-1]
+    assert (s.rows, s.cols, s.group) == (64, 128, 64)
+    if not pair:
+        last.biases = None
+        assert structs()[-1].biases is None

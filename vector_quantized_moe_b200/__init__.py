@@ -420,18 +420,33 @@ def _workspace(n, given, like):
 
 class Norm:
     """The weight of a root-mean-square norm (vq_norm): weight [hidden] fp32 or bf16; offset is 1 for checkpoints that
-    store weight - 1."""
+    store weight - 1. A call uses the weight as it is then: another one may be assigned, or new data to it."""
 
     def __init__(self, weight, eps: float = 1e-6, offset: float = 0.0):
         if _codes is None:
             _types()
         _L()
-        code = _codes.get(weight.dtype)
-        if code is None or weight.dim() != 1 or weight.numel() < 1 or not weight.is_contiguous():
-            _bad("Norm: weight")
-        self.weight, self.hidden = weight, weight.numel()
-        self._s = vq_norm(self.hidden, code, weight.data_ptr(), eps, offset)
+        self.weight = weight
+        self._s = vq_norm(0, 0, None, eps, offset)
         self._ref = ctypes.byref(self._s)
+        self._bind()
+
+    def _bind(self):
+        w, self._at = self.weight, None
+        code = _codes.get(w.dtype)
+        if code is None or w.dim() != 1 or w.numel() < 1 or not w.is_contiguous():
+            _bad("Norm: weight")
+        self.hidden, self._dtype = w.numel(), w.dtype
+        self._s.hidden, self._s.weight_dtype, self._s.weight = self.hidden, code, w.data_ptr()
+        self._at = w.data_ptr()
+
+    def _now(self):
+        """The struct of the weight as it is now."""
+        w = self.weight
+        if (w.data_ptr() != self._at or w.dtype is not self._dtype or w.numel() != self.hidden
+                or not w.is_contiguous()):
+            self._bind()
+        return self._ref
 
     def _held(self):
         return [self.weight]
@@ -441,6 +456,7 @@ def norm_pre(norm: Norm, h, out=None, stream=None):
     """x [T, hidden] bf16 = norm(h), the input of a block from the residual stream h (fp32 or bf16) (vq_norm_pre)."""
     if stream is not None:
         return _on_stream(stream, norm_pre, norm, h, out)
+    ref = norm._now()
     T, H = h.shape[0], norm.hidden
     hp, hd, hl = _row_arg("norm_pre: h", h, T, H)
     if out is None:
@@ -449,7 +465,7 @@ def norm_pre(norm: Norm, h, out=None, stream=None):
     else:
         xp, _, xl = _row_arg("norm_pre: out", out, T, H, VQ_BF16)
     dev = _one_device("norm_pre", h, norm.weight, out)
-    _launch("vq_norm_pre", dev, norm._ref, hp, hd, hl, T, xp, xl)
+    _launch("vq_norm_pre", dev, ref, hp, hd, hl, T, xp, xl)
     return out
 
 
@@ -470,6 +486,7 @@ def norm_pre_backward(norm: Norm, h, dx, dres=None, weight_grad: bool = True, wo
     norm, added to dh (vq_norm_pre_backward)."""
     if stream is not None:
         return _on_stream(stream, norm_pre_backward, norm, h, dx, dres, weight_grad, workspace)
+    ref = norm._now()
     T, H = h.shape[0], norm.hidden
     hp, hd, hl = _row_arg("norm_pre_backward: h", h, T, H)
     xp, _, xl = _row_arg("norm_pre_backward: dx", dx, T, H, VQ_BF16)
@@ -486,7 +503,7 @@ def norm_pre_backward(norm: Norm, h, dx, dres=None, weight_grad: bool = True, wo
         nb = _norm_ws(H, T)
         if nb:
             workspace, wp, nb = _workspace(nb, workspace, h)
-    _launch("vq_norm_pre_backward", dev, norm._ref, hp, hd, hl, xp, xl, rp, rl, T, dh.data_ptr(), H, dp, wp, nb)
+    _launch("vq_norm_pre_backward", dev, ref, hp, hd, hl, xp, xl, rp, rl, T, dh.data_ptr(), H, dp, wp, nb)
     return dh, dw
 
 
@@ -505,9 +522,10 @@ def _gate_arg(where, gate, T, H):
 
 
 def _norm_ref(where, norm, H):
+    ref = norm._now()
     if norm.hidden != H:
         _bad(where)
-    return norm._ref
+    return ref
 
 
 def norm_post(y, h, post: Optional[Norm] = None, gate=None, res_scale: float = 1.0, out_scale: float = 1.0,
@@ -664,7 +682,8 @@ def balance_loss_backward(logits, counts, top_k: int, dloss=None, mask=None, coe
 
 
 class Q4Module:
-    """A dense 4-bit matrix [rows, cols] with group scales on the device, in the kernel's tile layout (vq_q4_module)."""
+    """A dense 4-bit matrix [rows, cols] with group scales on the device, in the kernel's tile layout (vq_q4_module). A
+    call uses the arrays that the module has then."""
 
     def __init__(self, rows, cols, group, words, scales, biases=None):
         if _codes is None:
@@ -672,8 +691,19 @@ class Q4Module:
         _L()
         self.rows, self.cols, self.group = rows, cols, group
         self.words, self.scales, self.biases = words, scales, biases
-        self._s = vq_q4_module(rows, cols, group, _ptr(words), _ptr(scales), _ptr(biases))
+        self._s = vq_q4_module()
         self._ref = ctypes.byref(self._s)
+        self._at = None
+
+    def _now(self):
+        """The struct of the module as it is now."""
+        b = self.biases
+        at = (self.rows, self.cols, self.group, self.words.data_ptr(), self.scales.data_ptr(),
+              None if b is None else b.data_ptr())
+        if at != self._at:
+            s = self._s
+            s.rows, s.cols, s.group, s.words, s.scales, s.biases = self._at = at
+        return self._ref
 
     def _held(self):
         return [self.words, self.scales, self.biases]
@@ -714,6 +744,7 @@ def q4_gemv(m: Q4Module, x, up: Optional[Q4Module] = None, out_dtype=None, out=N
     or bfloat16 (the default, or out's)."""
     if stream is not None:
         return _on_stream(stream, q4_gemv, m, x, up, out_dtype, out)
+    ref, up_ref = m._now(), None if up is None else up._now()
     T, rows = x.shape[0], m.rows
     xp, _, xl = _row_arg("q4_gemv: x", x, T, m.cols, VQ_BF16)
     if out is None:
@@ -728,7 +759,7 @@ def q4_gemv(m: Q4Module, x, up: Optional[Q4Module] = None, out_dtype=None, out=N
             _bad("q4_gemv: out_dtype")
         yp, yd, yl = _row_arg("q4_gemv: out", out, T, rows)
         dev = _one_device("q4_gemv", x, m.words, out, None if up is None else up.words)
-    _launch("vq_q4_gemv", dev, m._ref, None if up is None else up._ref, xp, xl, T, yp, yd, yl)
+    _launch("vq_q4_gemv", dev, ref, up_ref, xp, xl, T, yp, yd, yl)
     return out
 
 
