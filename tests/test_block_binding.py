@@ -97,3 +97,57 @@ def test_a_4_bit_module_uses_the_arrays_it_has_at_the_call(launches, pair):
     if not pair:
         last.biases = None
         assert structs()[-1].biases is None
+
+
+def refused(f, *a, **k):
+    with pytest.raises(vq.VQError) as e:
+        f(*a, **k)
+    assert e.value.status == ARG
+
+
+@pytest.mark.parametrize("change", [
+    dict(words=slice(0, -1)), dict(words=slice(0, 256)), dict(scales=slice(0, 16)), dict(biases=slice(0, -8)),
+    dict(words=BF16), dict(scales=BF16), dict(biases=F32), dict(words=slice(None, None, 2)), dict(rows=80), dict(cols=256),
+    dict(group=32), dict(rows=0), dict(group=48), dict(cols=96)])
+@pytest.mark.parametrize("as_up", [False, True])
+@pytest.mark.parametrize("late", [False, True])
+def test_a_4_bit_module_that_does_not_hold_its_layout_is_refused(launches, change, as_up, late):
+    # before the first call, and after calls that were right
+    rows, cols = 64, 128
+    m, other = (vq.Q4Module(rows, cols, 64, *q4_arrays(rows, cols, 64, True)) for _ in range(2))
+    x = torch.zeros((2, cols), dtype=BF16)
+    call = (lambda: vq.q4_gemv(other, x, m)) if as_up else (lambda: vq.q4_gemv(m, x))
+    if late:
+        call()
+    for name, what in change.items():
+        old = getattr(m, name)
+        if isinstance(what, slice):
+            # steps: as many elements as the layout has, but not consecutive
+            new = old.repeat(2)[what] if what.step else old[what]
+        else:
+            new = torch.zeros(old.shape, dtype=what) if isinstance(what, torch.dtype) else what
+        setattr(m, name, new)
+    launches.clear()
+    refused(call)
+    refused(call)
+    assert not launches
+
+
+def test_a_4_bit_module_checks_all_its_arrays_devices(monkeypatch):
+    seen = []
+    monkeypatch.setattr(vq, "_one_device", lambda where, first, *others: seen.extend((first, *others)) or 0)
+    monkeypatch.setattr(vq, "_launch", lambda *a: None)
+    m = vq.Q4Module(64, 128, 64, *q4_arrays(64, 128, 64, True))
+    x = torch.zeros((2, 128), dtype=BF16)
+    vq.q4_gemv(m, x)
+    assert all(any(t is s for s in seen) for t in (x, m.words, m.scales, m.biases))
+    for out in (None, torch.zeros((2, 64), dtype=BF16)):
+        m._dev = 1   # a module on another GPU than the tokens
+        refused(vq.q4_gemv, m, x, out=out)
+
+
+def test_an_undersized_module_is_refused_before_any_gpu_is_asked_for():
+    m = vq.Q4Module(64, 64, 64, torch.zeros(256, dtype=torch.int32), torch.zeros(16, dtype=torch.int16))
+    refused(vq.q4_gemv, m, torch.zeros((2, 64), dtype=BF16))
+    with pytest.raises(vq.VQError, match="words"):
+        m._now()

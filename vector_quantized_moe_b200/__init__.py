@@ -682,8 +682,9 @@ def balance_loss_backward(logits, counts, top_k: int, dloss=None, mask=None, coe
 
 
 class Q4Module:
-    """A dense 4-bit matrix [rows, cols] with group scales on the device, in the kernel's tile layout (vq_q4_module). A
-    call uses the arrays that the module has then."""
+    """A dense 4-bit matrix [rows, cols] with group scales on the device, in the kernel's tile layout (vq_q4_module):
+    at least vq_q4_packed_words int32 words, vq_q4_packed_scales fp16 scales (or their int16 bits), and as many biases, as
+    from_rows makes them. A call checks and uses the arrays that the module has then."""
 
     def __init__(self, rows, cols, group, words, scales, biases=None):
         if _codes is None:
@@ -697,13 +698,30 @@ class Q4Module:
 
     def _now(self):
         """The struct of the module as it is now."""
-        b = self.biases
-        at = (self.rows, self.cols, self.group, self.words.data_ptr(), self.scales.data_ptr(),
-              None if b is None else b.data_ptr())
+        w, s, b = self.words, self.scales, self.biases
+        at = (self.rows, self.cols, self.group, w.data_ptr(), s.data_ptr(), None if b is None else b.data_ptr(),
+              w.numel(), s.numel(), None if b is None else b.numel())
         if at != self._at:
-            s = self._s
-            s.rows, s.cols, s.group, s.words, s.scales, s.biases = self._at = at
+            self._bind(at)
         return self._ref
+
+    def _bind(self, at):
+        self._at = None
+        rows, cols, group, *pointers = at[:6]
+        nw, ns = int(_L().vq_q4_packed_words(rows, cols)), int(_L().vq_q4_packed_scales(rows, cols, group))
+        if nw == 0 or ns == 0:
+            _bad("Q4Module: rows, cols, group")
+        torch = _torch()
+        for name, t, n, types in (("words", self.words, nw, (torch.int32, torch.uint32)),
+                                  ("scales", self.scales, ns, (torch.int16, torch.float16)),
+                                  ("biases", self.biases, ns, (torch.int16, torch.float16))):
+            if t is not None and (t.dtype not in types or t.numel() < n or not t.is_contiguous()):
+                _bad("Q4Module: " + name)
+        self._dev = _one_device("Q4Module", self.words, self.scales, self.biases)
+        s = self._s
+        s.rows, s.cols, s.group = rows, cols, group
+        s.words, s.scales, s.biases = pointers
+        self._at = at
 
     def _held(self):
         return [self.words, self.scales, self.biases]
@@ -751,14 +769,16 @@ def q4_gemv(m: Q4Module, x, up: Optional[Q4Module] = None, out_dtype=None, out=N
         yd = VQ_BF16 if out_dtype is None else _codes.get(out_dtype)
         if yd is None:
             _bad("q4_gemv: out_dtype")
-        dev = _one_device("q4_gemv", x, m.words, None if up is None else up.words)
+        dev = _one_device("q4_gemv", x)
         out = x.new_empty((T, rows), dtype=out_dtype or _bf16)
         yp, yl = out.data_ptr(), rows
     else:
         if out_dtype is not None and out.dtype != out_dtype:
             _bad("q4_gemv: out_dtype")
         yp, yd, yl = _row_arg("q4_gemv: out", out, T, rows)
-        dev = _one_device("q4_gemv", x, m.words, out, None if up is None else up.words)
+        dev = _one_device("q4_gemv", x, out)
+    if dev != m._dev or (up is not None and dev != up._dev):
+        _bad("q4_gemv (module on another device)")
     _launch("vq_q4_gemv", dev, ref, up_ref, xp, xl, T, yp, yd, yl)
     return out
 
