@@ -203,6 +203,17 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _workspace(n, given, like):
+    """(tensor, aligned pointer, bytes) of a workspace of n bytes for a call on `like`: the given one, which has to be
+    one piece on like's device, or a new one. The bytes are those behind the aligned pointer, 0 when there are none."""
+    ws = given if given is not None else like.new_empty(n + 256, dtype=_torch().uint8)
+    if not ws.is_contiguous() or ws.get_device() != like.get_device():
+        raise VQError(VQ_ERR_ARG, "workspace")
+    base = ws.data_ptr()
+    aligned = (base + 255) // 256 * 256
+    return ws, aligned, max(0, ws.numel() * ws.element_size() - (aligned - base))
+
+
 class Module:
     """One VQ module on the device (vq_module). Tensors are kept alive here."""
 
@@ -282,11 +293,9 @@ def gemm(m0: Module, expert: int, x, m1: Optional[Module] = None, workspace=None
     n = int(_L().vq_gemm_workspace_size(ctypes.byref(s0), T))
     if n == 0:
         raise VQError(VQ_ERR_ARG, "vq_gemm_workspace_size")
-    ws = workspace if workspace is not None else torch.empty(n + 256, dtype=torch.uint8, device=x.device)
-    base = ws.data_ptr()
-    aligned = (base + 255) // 256 * 256
+    ws, aligned, nbytes = _workspace(n, workspace, x)
     _check(_L().vq_gemm(ctypes.byref(s0), None if s1 is None else ctypes.byref(s1), expert, x.data_ptr(), T,
-                        y0.data_ptr(), _ptr(y1), aligned, ws.numel() - (aligned - base), _stream(stream)), "vq_gemm")
+                        y0.data_ptr(), _ptr(y1), aligned, nbytes, _stream(stream)), "vq_gemm")
     return y0, y1, ws
 
 
@@ -318,19 +327,19 @@ def fit(w, d: int, K: int, sample, init, iters: int, workspace=None, stream=None
     n = int(_L().vq_fit_workspace_size(K, d))
     if n == 0:
         raise VQError(1, "vq_fit_workspace_size")
-    ws = workspace if workspace is not None else torch.empty(n + 256, dtype=torch.uint8, device=dev)
-    base = ws.data_ptr()
-    aligned = (base + 255) // 256 * 256
+    ws, aligned, nbytes = _workspace(n, workspace, w)
     _check(_L().vq_fit(w.data_ptr(), rows, cols, d, K, sample.data_ptr(), sample.numel(), init.data_ptr(), iters,
-                       scales.data_ptr(), codebook.data_ptr(), codes.data_ptr(), aligned, ws.numel() - (aligned - base),
-                       _stream(stream)), "vq_fit")
+                       scales.data_ptr(), codebook.data_ptr(), codes.data_ptr(), aligned, nbytes, _stream(stream)),
+           "vq_fit")
     return scales, codebook, codes, ws
 
 
 def fit_check(workspace, stream=None) -> int:
     """Status of the error word of a vq_fit workspace returned by fit() (vq_moe_check)."""
-    base = (workspace.data_ptr() + 255) // 256 * 256
-    return int(_L().vq_moe_check(base, _stream(stream)))
+    _, aligned, nbytes = _workspace(0, workspace, workspace)
+    if nbytes < 4:
+        raise VQError(VQ_ERR_WORKSPACE, "fit_check")
+    return int(_L().vq_moe_check(aligned, _stream(stream)))
 
 
 # ------------------------------------------------------------------ the block around the experts
@@ -406,16 +415,6 @@ def _one_device(where, first, *others) -> int:
         if t is not None and t.get_device() != dev:
             _bad(where + " (tensors on different devices)")
     return dev
-
-
-def _workspace(n, given, like):
-    """(tensor, aligned pointer, bytes) of a workspace of n bytes: the given one, or a new one on like's device."""
-    ws = given if given is not None else like.new_empty(n + 256, dtype=_torch().uint8)
-    if not ws.is_contiguous():
-        _bad("workspace")
-    base = ws.data_ptr()
-    aligned = (base + 255) // 256 * 256
-    return ws, aligned, max(0, ws.numel() * ws.element_size() - (aligned - base))
 
 
 class Norm:
@@ -838,9 +837,7 @@ class MoELayer:
         if out is None:
             out = torch.empty((T, self.hidden), dtype=out_dtype or torch.float32, device=x.device)
         ws = workspace if workspace is not None else self.workspace(T, top_k, mode, x.device)
-        base = ws.data_ptr()
-        aligned = (base + 255) // 256 * 256
-        nbytes = ws.numel() - (aligned - base)
+        _, aligned, nbytes = _workspace(0, ws, x)
         _check(fn(ctypes.byref(self._s), x.data_ptr(), T, logits.data_ptr(), top_k, int(bool(renorm)),
                   out.data_ptr(), _dt(out.dtype), aligned, nbytes, _stream(stream)), name)
         return out
@@ -875,9 +872,7 @@ class MoELayer:
             out = torch.empty((T, self.hidden), dtype=out_dtype or torch.float32, device=x.device)
         ws = workspace if workspace is not None else self.workspace(max(1, min(T, chunk)), top_k, VQ_MODE_PREFILL,
                                                                      x.device)
-        base = ws.data_ptr()
-        aligned = (base + 255) // 256 * 256
-        nbytes = ws.numel() - (aligned - base)
+        _, aligned, nbytes = _workspace(0, ws, x)
         _check(_L().vq_moe_prefill_chunked(ctypes.byref(self._s), x.data_ptr(), T, logits.data_ptr(), top_k,
                                             int(bool(renorm)), int(chunk), out.data_ptr(), _dt(out.dtype), aligned,
                                             nbytes, _stream(stream)), "vq_moe_prefill_chunked")
