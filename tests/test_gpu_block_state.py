@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import vector_quantized_moe_b200 as vq
+from helpers import lib_module, small_module
 from test_gpu_q4 import module, tokens
 
 pytestmark = pytest.mark.gpu
@@ -32,3 +33,39 @@ def test_a_4_bit_module_with_other_arrays():
     assert not torch.equal(vq.q4_gemv(m, x), want)
     m.words, m.scales, m.biases = other.words.clone(), other.scales.clone(), other.biases.clone()
     assert torch.equal(vq.q4_gemv(m, x), want)
+
+
+def layer_of(E, H, I, seed):
+    return vq.MoELayer(*[lib_module(small_module(E, r, c, 2, 8, seed=seed + i))
+                         for i, (r, c) in enumerate(((I, H), (I, H), (H, I)))])
+
+
+@pytest.mark.parametrize("T", [1, 8, 200, 700])
+@pytest.mark.parametrize("path", ["decode", "prefill"])
+@pytest.mark.parametrize("writer", ["pre", "post"])
+def test_x_rewritten_by_the_call_before_the_experts(T, path, writer):
+    # the experts read the x that the launch before them wrote over the one that the calls before that have read
+    E, H, I, K = 8, 512, 256, 2
+    layer, n = layer_of(E, H, I, 40), vq.Norm(torch.ones(H, device="cuda"))
+    _, m = module(64, H, 64, False, 43)
+    g = torch.Generator().manual_seed(44)
+    hs = [torch.randn((T, H), generator=g).cuda() for _ in range(12)]
+    logits = torch.randn((T, E), generator=g).cuda()
+    zero = torch.zeros_like(hs[0])
+    experts = getattr(layer, path)
+    xs = [vq.norm_pre(n, h) for h in hs]
+    want = []
+    for x in xs:
+        torch.cuda.synchronize()
+        want.append((experts(x, logits, K), vq.q4_gemv(m, x)))
+    x, got = torch.empty_like(xs[0]), []
+    torch.cuda.synchronize()
+    for h in hs:
+        if writer == "pre":
+            vq.norm_pre(n, h, out=x)
+        else:
+            vq.norm_post(zero, h, next=n, x_out=x)
+        y = experts(x, logits, K)
+        got.append((y, vq.q4_gemv(m, x)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for p, q in zip(got, want) for a, b in zip(p, q))

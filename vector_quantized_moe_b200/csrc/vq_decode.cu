@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(GEMV_THREADS, 2) vq_grouped_gemv_kernel(const 
             auto compute = [&](const GroupLoads<D, BITS> &L, int grp) {
                 uint4 av0 = make_uint4(0u, 0u, 0u, 0u), av1 = av0;
                 if (has_tok) {
-                    av0 = ldg_u128(arow + (long)grp * 64);
-                    av1 = ldg_u128(arow + (long)grp * 64 + 8);
+                    av0 = load_u128(arow + (long)grp * 64);
+                    av1 = load_u128(arow + (long)grp * 64 + 8);
                 }
                 uint32_t bw[8] = {av0.x, av0.y, av0.z, av0.w, av1.x, av1.y, av1.z, av1.w};
                 float f0 = 1.f, f1 = 1.f;   // inverse activation scales of the fragment's token columns
@@ -1096,9 +1096,8 @@ constexpr int SWIGLU_KEEP = 8;
 
 template <int S>
 __global__ void __launch_bounds__(SWIGLU_THREADS) vq_swiglu_kernel(
-    const float *__restrict__ G, const float *__restrict__ U, int slices, long slice_stride, int slots, int inter,
-    const int32_t *__restrict__ perm, int top_k, const float *__restrict__ xinv, const float *__restrict__ w,
-    __half *__restrict__ h, float *__restrict__ wh)
+    const float *G, const float *U, int slices, long slice_stride, int slots, int inter, const int32_t *perm, int top_k,
+    const float *xinv, const float *w, __half *__restrict__ h, float *__restrict__ wh)
 {
     __shared__ uint32_t red[SWIGLU_THREADS / 32];
     grid_dep_launch();   // the next kernel may start its prologue; it waits for this one's results
@@ -1171,9 +1170,9 @@ __global__ void __launch_bounds__(SWIGLU_THREADS) vq_swiglu_kernel(
 // columns per thread. The loads of 8 slots x S slices are issued before any
 // is used.
 template <int S>
-__global__ void __launch_bounds__(256) vq_combine_kernel(const float *__restrict__ D, int slices, long slice_stride,
-                                                         const float *__restrict__ w, const int32_t *__restrict__ pos,
-                                                         int T, int k, int hidden, void *y, int y_dtype)
+__global__ void __launch_bounds__(256) vq_combine_kernel(const float *D, int slices, long slice_stride,
+                                                         const float *w, const int32_t *pos, int T, int k, int hidden,
+                                                         void *__restrict__ y, int y_dtype)
 {
     __shared__ long q_s[32];
     __shared__ float w_s[32];

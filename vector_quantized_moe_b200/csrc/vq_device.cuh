@@ -23,18 +23,21 @@ __device__ __forceinline__ uint2 ldg_u64(const uint32_t *p)
     return v;
 }
 
-__device__ __forceinline__ uint4 ldg_u128(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-
 __device__ __forceinline__ uint16_t ldg_u16(const uint16_t *p)
 {
     unsigned short v;
     asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+
+// Activations and everything else that an earlier launch of the path writes: an ordinary load. A kernel launched
+// programmatically may sit on an SM while that launch still writes, and the read-only path asks for data that no one
+// writes while the kernel runs. For the same reason such inputs carry no __restrict__, which would let the compiler
+// choose the read-only path.
+__device__ __forceinline__ uint4 load_u128(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 

@@ -733,8 +733,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) vq_prefill_gemm_kernel(const __gr
 
 // gathered activations: Xg[q, :] = x16[perm[q] / k, :] (the token's scaled fp16
 // row) and sxinv[q] = xinv[perm[q] / k] (its inverse scale)
-__global__ void vq_gather_kernel(const __half *__restrict__ x16, const float *__restrict__ xinv,
-                                 const int32_t *__restrict__ perm, int k, long slots, int H, __half *__restrict__ xg,
+__global__ void vq_gather_kernel(const __half *x16, const float *xinv, const int32_t *perm, int k, long slots, int H,
+                                 __half *__restrict__ xg,
                                  float *__restrict__ sxinv)
 {
     grid_dep_launch();   // the next kernel may start its prologue; it waits for this one's results
@@ -744,7 +744,7 @@ __global__ void vq_gather_kernel(const __half *__restrict__ x16, const float *__
         const long q = i / per_row;
         const int c = (int)(i % per_row) * 8;
         const long t = perm[q] / k;
-        *reinterpret_cast<uint4 *>(xg + q * H + c) = ldg_u128(x16 + t * H + c);
+        *reinterpret_cast<uint4 *>(xg + q * H + c) = load_u128(x16 + t * H + c);
         if (c == 0)
             sxinv[q] = xinv[t];
     }
@@ -758,8 +758,8 @@ __global__ void vq_gather_kernel(const __half *__restrict__ x16, const float *__
 // that the combine applies to the down projection. One warp per slot; the
 // lanes take consecutive 16-byte chunks of the row, so each load and store of
 // the warp covers 512 contiguous bytes.
-__global__ void vq_hnorm_kernel(__half *__restrict__ h, const int8_t *__restrict__ hexp, long slots, int nblk,
-                                const int32_t *__restrict__ perm, const float *__restrict__ w, float *__restrict__ wh)
+__global__ void vq_hnorm_kernel(__half *__restrict__ h, const int8_t *hexp, long slots, int nblk, const int32_t *perm,
+                                const float *w, float *__restrict__ wh)
 {
     grid_dep_launch();   // the next kernel may start its prologue; it waits for this one's results
     grid_dep_wait();

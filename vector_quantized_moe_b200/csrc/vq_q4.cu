@@ -109,14 +109,6 @@ __device__ __forceinline__ void sts128(uint32_t at, uint4 v)
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Not a read-only load: x may be the work of the launch before, which ends only after this one has started.
-__device__ __forceinline__ uint4 load128(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-
 template <int NG>
 __device__ __forceinline__ void lds_pairs(uint32_t at, uint32_t (&v)[NG])
 {
@@ -210,7 +202,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS<R, NT>, MIN_CTAS<R, NT>) vq_q4_
         const int k = min(sb * 128 + p * 32, a.cols - 32);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            v[n] = load128(xp[n] + k);
+            v[n] = load_u128(xp[n] + k);
     };
     if constexpr (X_RING<R>) {   // chunks that no copy fills hold zeros
         if (a.cols % 128)

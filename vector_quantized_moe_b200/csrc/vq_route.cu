@@ -305,7 +305,7 @@ __device__ void convert_rows(const uint16_t *x, __half *x16, float *xinv, int t0
             uint4 v[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                v[u] = i0 + 32 * u < n8 ? ldg_u128(src + i0 + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
+                v[u] = i0 + 32 * u < n8 ? load_u128(src + i0 + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int u = 0; u < 8; ++u)
                 m = max(m, bf16x8_max_mag(v[u]));
@@ -320,7 +320,7 @@ __device__ void convert_rows(const uint16_t *x, __half *x16, float *xinv, int t0
 #pragma unroll
             for (int u = 0; u < 8; ++u)
                 if (i0 + 32 * u < n8)
-                    v[u] = ldg_u128(src + i0 + 32 * u);
+                    v[u] = load_u128(src + i0 + 32 * u);
 #pragma unroll
             for (int u = 0; u < 8; ++u)
                 if (i0 + 32 * u < n8) {
