@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import vector_quantized_moe_b200 as vq
+from helpers import lib_module, small_module
 
 BF16, F32 = torch.bfloat16, torch.float32
 ARG, WORKSPACE = 1, 4
@@ -151,3 +152,31 @@ def test_an_undersized_module_is_refused_before_any_gpu_is_asked_for():
     refused(vq.q4_gemv, m, torch.zeros((2, 64), dtype=BF16))
     with pytest.raises(vq.VQError, match="words"):
         m._now()
+
+
+@pytest.fixture
+def block(launches, monkeypatch):
+    """A block on CPU tensors that pass for GPU 0's; its experts record the x they get."""
+    E, H, I = 4, 512, 256
+    layer = vq.MoELayer(*[lib_module(small_module(E, r, c, 2, 8, seed=i), device="cpu")
+                          for i, (r, c) in enumerate(((I, H), (I, H), (H, I)))])
+    layer._dev = 0
+    seen = []
+    layer.decode = layer.prefill = lambda x, *a, **k: seen.append(x) or torch.zeros((x.shape[0], H))
+    monkeypatch.setattr(vq, "_device", lambda: 0)
+    b = vq.MoEBlock(layer, vq.Norm(torch.ones(H)), lambda x: torch.zeros((x.shape[0], E)), 2)
+    b.seen = seen
+    return b
+
+
+@pytest.mark.parametrize("path", ["decode", "prefill"])
+def test_experts_get_rows_of_their_own_width_only(block, path):
+    run = getattr(block, path)
+    run(torch.zeros((3, 512)), torch.zeros((3, 512), dtype=BF16))
+    assert len(block.seen) == 1
+    for width in (256, 1024):   # h and a given x agree with each other, and a router that looks at neither
+        refused(run, torch.zeros((3, width)), torch.zeros((3, width), dtype=BF16))
+    refused(run, torch.zeros(512), torch.zeros(512, dtype=BF16))
+    block.pre = vq.Norm(torch.ones(256))   # a norm of another width, given later
+    refused(run, torch.zeros((3, 256)))
+    assert len(block.seen) == 1

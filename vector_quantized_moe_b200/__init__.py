@@ -913,6 +913,8 @@ class MoEBlock:
         if dev != _device():
             with _torch().cuda.device(dev):
                 return self._run(experts, mode, h, x, workspace)
+        if h.dim() != 2 or h.shape[1] != self.layer.hidden:   # the experts read rows of hidden elements of x
+            _bad("MoEBlock: h")
         if x is None:
             x = norm_pre(self.pre, h)
         elif x.dtype is not _bf16 or x.shape != h.shape or not x.is_contiguous():
