@@ -180,3 +180,34 @@ def test_experts_get_rows_of_their_own_width_only(block, path):
     block.pre = vq.Norm(torch.ones(256))   # a norm of another width, given later
     refused(run, torch.zeros((3, 256)))
     assert len(block.seen) == 1
+
+
+@pytest.mark.parametrize("path", ["decode", "prefill"])
+def test_experts_on_another_device_are_refused(block, path):
+    block.layer._dev = 1
+    refused(getattr(block, path), torch.zeros((3, 512)))
+    assert not block.seen
+
+
+class OnGPU:
+    """A tensor that says it is on GPU 3."""
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return 3
+
+
+def test_a_layer_knows_the_one_device_of_its_arrays():
+    mods = [lib_module(small_module(4, r, c, 2, 8, seed=i), device="cpu")
+            for i, (r, c) in enumerate(((256, 512), (256, 512), (512, 256)))]
+    assert vq.MoELayer(*mods)._dev == -1
+    for name in ("codes", "scales", "codebook"):
+        old = getattr(mods[2], name)
+        setattr(mods[2], name, OnGPU(old))
+        assert vq.MoELayer(*mods)._dev is None
+        setattr(mods[2], name, old)

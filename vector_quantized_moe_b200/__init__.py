@@ -815,6 +815,9 @@ class MoELayer:
         self.hidden, self.inter, self.E = gate.cols, gate.rows, gate.E
         self._s = vq_moe_layer(gate.struct(), up.struct(), down.struct())
         self._ws = {}
+        devs = {t.get_device() for m in (gate, up, down)
+                for t in (m.codes, m.scales, m.codebook, m.live_bitmap, m.live_rank, m.biases) if t is not None}
+        self._dev = devs.pop() if len(devs) == 1 else None   # index of the one GPU that all arrays are on
 
     def workspace_size(self, T: int, top_k: int, mode: int) -> int:
         return int(_L().vq_moe_workspace_size(ctypes.byref(self._s), T, top_k, mode))
@@ -913,6 +916,8 @@ class MoEBlock:
         if dev != _device():
             with _torch().cuda.device(dev):
                 return self._run(experts, mode, h, x, workspace)
+        if dev != self.layer._dev:
+            _bad("MoEBlock (layer on another device)")
         if h.dim() != 2 or h.shape[1] != self.layer.hidden:   # the experts read rows of hidden elements of x
             _bad("MoEBlock: h")
         if x is None:
