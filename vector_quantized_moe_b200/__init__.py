@@ -350,14 +350,14 @@ def fit_check(workspace, stream=None) -> int:
 # (VQError with VQ_ERR_ARG) before it launches and runs on its tensors' device: on that device's current stream, or on
 # `stream` when one is given (the outputs then belong to that stream).
 
-_bf16 = _f32 = _codes = _device = _raw_stream = None
+_bf16 = _f32 = _codes = _device = _raw_stream = _empty_like = None
 
 
 def _types():
     """Binds what the calls below use of torch once (they are on a decode step's host path)."""
-    global _bf16, _f32, _codes, _device, _raw_stream
+    global _bf16, _f32, _codes, _device, _raw_stream, _empty_like
     torch = _torch()
-    _bf16, _f32 = torch.bfloat16, torch.float32
+    _bf16, _f32, _empty_like = torch.bfloat16, torch.float32, torch.empty_like
     _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _codes = {torch.float32: VQ_F32, torch.bfloat16: VQ_BF16, torch.int16: VQ_BF16}
 
@@ -400,6 +400,8 @@ def _row_arg(where, t, T, cols, like=None):
     code = _codes.get(t.dtype)
     if code is None or (like is not None and code != like) or t.shape != (T, cols):
         _bad(where)
+    if t.is_contiguous():
+        return t.data_ptr(), code, cols
     ld, inner = t.stride()
     if (cols > 1 and inner != 1) or (T > 1 and ld < cols):
         _bad(where)
@@ -430,8 +432,13 @@ class Norm:
         self._ref = ctypes.byref(self._s)
         self._bind()
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name[0] != "_":
+            self._at = None   # not bound
+
     def _bind(self):
-        w, self._at = self.weight, None
+        w = self.weight
         code = _codes.get(w.dtype)
         if code is None or w.dim() != 1 or w.numel() < 1 or not w.is_contiguous():
             _bad("Norm: weight")
@@ -444,6 +451,7 @@ class Norm:
         w = self.weight
         if (w.data_ptr() != self._at or w.dtype is not self._dtype or w.numel() != self.hidden
                 or not w.is_contiguous()):
+            self._at = None
             self._bind()
         return self._ref
 
@@ -455,24 +463,22 @@ def norm_pre(norm: Norm, h, out=None, stream=None):
     """x [T, hidden] bf16 = norm(h), the input of a block from the residual stream h (fp32 or bf16) (vq_norm_pre)."""
     if stream is not None:
         return _on_stream(stream, norm_pre, norm, h, out)
-    ref = norm._now()
-    T, H = h.shape[0], norm.hidden
+    ref, H, T = norm._now(), norm.hidden, h.shape[0]
     hp, hd, hl = _row_arg("norm_pre: h", h, T, H)
+    dev = _one_device("norm_pre", h, norm.weight, out)
     if out is None:
         out = _empty(h, _bf16)
         xp, xl = out.data_ptr(), H
     else:
         xp, _, xl = _row_arg("norm_pre: out", out, T, H, VQ_BF16)
-    dev = _one_device("norm_pre", h, norm.weight, out)
     _launch("vq_norm_pre", dev, ref, hp, hd, hl, T, xp, xl)
     return out
 
 
 def _empty(like, dtype):
-    """A new contiguous array of like's shape on its device."""
-    if like.dtype is dtype:
-        return _torch().empty_like(like)
-    return like.new_empty(like.shape, dtype=dtype)
+    """A new array of like's shape on its device, rows one after the other (like's own elements are consecutive in a
+    row, so that empty_like either keeps them so or, for a window, makes them so; it takes half of new_empty's time)."""
+    return _empty_like(like) if like.dtype is dtype else _empty_like(like, dtype=dtype)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -550,6 +556,8 @@ def norm_post(y, h, post: Optional[Norm] = None, gate=None, res_scale: float = 1
         pr, w1 = _norm_ref("norm_post: post", post, H), post.weight
     if next is not None:
         nr, w2 = _norm_ref("norm_post: next", next, H), next.weight
+    dev = _one_device("norm_post", y, h, gate, h_out, x_out, w1, w2)
+    if next is not None:
         if x_out is None:
             x_out = _empty(h, _bf16)
             xp, xl = x_out.data_ptr(), H
@@ -562,7 +570,6 @@ def norm_post(y, h, post: Optional[Norm] = None, gate=None, res_scale: float = 1
         op, ol = h_out.data_ptr(), H
     else:
         op, _, ol = _row_arg("norm_post: h_out", h_out, T, H, hd)
-    dev = _one_device("norm_post", y, h, gate, h_out, x_out, w1, w2)
     _launch("vq_norm_post", dev, pr, nr, H, yp, yd, yl, gp, gd, gc, gl, hp, hd, hl, res_scale, out_scale, T, op, ol, xp, xl)
     return h_out, x_out
 
@@ -600,7 +607,7 @@ def norm_post_backward(y, h_out, dh_out, dx_out=None, post: Optional[Norm] = Non
     dy = _empty(y, _f32 if yd == VQ_F32 else _bf16)
     dh = _empty(h_out, _f32 if hd == VQ_F32 else _bf16)
     if gate is not None:
-        dgate = gate.new_empty(gate.shape, dtype=_f32 if gd == VQ_F32 else _bf16)
+        dgate = _empty(gate, _f32 if gd == VQ_F32 else _bf16)
         zp = dgate.data_ptr()
     if post is not None:
         dpost = _empty(w1, _f32)
@@ -693,20 +700,27 @@ class Q4Module:
         self.words, self.scales, self.biases = words, scales, biases
         self._s = vq_q4_module()
         self._ref = ctypes.byref(self._s)
-        self._at = None
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name[0] != "_":
+            self._at = None   # not bound
 
     def _now(self):
         """The struct of the module as it is now."""
         w, s, b = self.words, self.scales, self.biases
-        at = (self.rows, self.cols, self.group, w.data_ptr(), s.data_ptr(), None if b is None else b.data_ptr(),
-              w.numel(), s.numel(), None if b is None else b.numel())
+        if b is None:
+            at = (w.data_ptr(), s.data_ptr(), w.numel(), s.numel())
+        else:
+            at = (w.data_ptr(), s.data_ptr(), w.numel(), s.numel(), b.data_ptr(), b.numel())
         if at != self._at:
-            self._bind(at)
+            self._at = None
+            self._bind()
+            self._at = at
         return self._ref
 
-    def _bind(self, at):
-        self._at = None
-        rows, cols, group, *pointers = at[:6]
+    def _bind(self):
+        rows, cols, group = self.rows, self.cols, self.group
         nw, ns = int(_L().vq_q4_packed_words(rows, cols)), int(_L().vq_q4_packed_scales(rows, cols, group))
         if nw == 0 or ns == 0:
             _bad("Q4Module: rows, cols, group")
@@ -719,8 +733,7 @@ class Q4Module:
         self._dev = _one_device("Q4Module", self.words, self.scales, self.biases)
         s = self._s
         s.rows, s.cols, s.group = rows, cols, group
-        s.words, s.scales, s.biases = pointers
-        self._at = at
+        s.words, s.scales, s.biases = _ptr(self.words), _ptr(self.scales), _ptr(self.biases)
 
     def _held(self):
         return [self.words, self.scales, self.biases]
@@ -769,7 +782,7 @@ def q4_gemv(m: Q4Module, x, up: Optional[Q4Module] = None, out_dtype=None, out=N
         if yd is None:
             _bad("q4_gemv: out_dtype")
         dev = _one_device("q4_gemv", x)
-        out = x.new_empty((T, rows), dtype=out_dtype or _bf16)
+        out = x.new_empty(T, rows, dtype=out_dtype or _bf16)
         yp, yl = out.data_ptr(), rows
     else:
         if out_dtype is not None and out.dtype != out_dtype:
