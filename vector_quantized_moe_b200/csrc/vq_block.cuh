@@ -69,7 +69,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a
 
 // ---------------------------------------------------------------- chunks of a row
 //
-// VEC consecutive elements of a row: 8 with 16-byte accesses, or 1.
+// VEC consecutive elements of a row: 8 with 16-byte accesses, as four fp32 pairs, or 1 (read only).
 
 template <typename T, int VEC>
 struct Chunk;
@@ -78,25 +78,6 @@ template <>
 struct Chunk<uint16_t, 8> {   // bf16
     uint4 r;
     __device__ __forceinline__ void load(const uint16_t *p) { r = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void get(float (&v)[8]) const
-    {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-    __device__ __forceinline__ void set(const float (&v)[8])
-    {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&b);
-        }
-        r = make_uint4(w[0], w[1], w[2], w[3]);
-    }
     __device__ __forceinline__ void store(uint16_t *p) const { *reinterpret_cast<uint4 *>(p) = r; }
     __device__ __forceinline__ void get(float2 (&v)[4]) const
     {
@@ -125,16 +106,6 @@ struct Chunk<float, 8> {
         a = reinterpret_cast<const float4 *>(p)[0];
         b = reinterpret_cast<const float4 *>(p)[1];
     }
-    __device__ __forceinline__ void get(float (&v)[8]) const
-    {
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
-    __device__ __forceinline__ void set(const float (&v)[8])
-    {
-        a = make_float4(v[0], v[1], v[2], v[3]);
-        b = make_float4(v[4], v[5], v[6], v[7]);
-    }
     __device__ __forceinline__ void store(float *p) const
     {
         reinterpret_cast<float4 *>(p)[0] = a;
@@ -157,8 +128,6 @@ struct Chunk<uint16_t, 1> {
     uint16_t r;
     __device__ __forceinline__ void load(const uint16_t *p) { r = *p; }
     __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = bf16_to_f32(r); }
-    __device__ __forceinline__ void set(const float (&v)[1]) { r = f32_to_bf16_bits(v[0]); }
-    __device__ __forceinline__ void store(uint16_t *p) const { *p = r; }
 };
 
 template <>
@@ -166,8 +135,6 @@ struct Chunk<float, 1> {
     float r;
     __device__ __forceinline__ void load(const float *p) { r = *p; }
     __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = r; }
-    __device__ __forceinline__ void set(const float (&v)[1]) { r = v[0]; }
-    __device__ __forceinline__ void store(float *p) const { *p = r; }
 };
 
 // A chunk whose type is known at run time (norm weights, per-channel gates):
@@ -183,14 +150,8 @@ struct AnyChunk {
         else
             h.load(static_cast<const uint16_t *>(p) + i);
     }
-    __device__ __forceinline__ void get(float (&v)[VEC], int dtype) const
-    {
-        if (dtype == VQ_F32)
-            f.get(v);
-        else
-            h.get(v);
-    }
-    __device__ __forceinline__ void get(float2 (&v)[VEC / 2], int dtype) const
+    template <typename V>
+    __device__ __forceinline__ void get(V &v, int dtype) const
     {
         if (dtype == VQ_F32)
             f.get(v);
@@ -311,13 +272,14 @@ __device__ __forceinline__ float warp_total_from(float v)
     return v;
 }
 
-// Sums of N <= 3 values over the W warps of a row, in a fixed order; rows side
+// Sums of N <= 3 values over the W <= 16 warps of a row, in a fixed order; rows side
 // by side in a CTA meet at barriers of their own. Several values share the warp's shuffles: 5, 5 and
 // 6 for 1, 2 and 3 values. Two buffers in turn: a warp may start the next sum
 // while another still reads this one.
+constexpr int ROW_THREADS = 512;           // most threads a row, and a CTA of rows
 template <int N>
 struct RowSum {
-    float buf[2][N][32];
+    float buf[2][N][ROW_THREADS / 32];
 };
 
 // A thread's place among the W warps of its row, R rows side by side in the CTA.
@@ -357,21 +319,15 @@ __device__ __forceinline__ void row_sum(float (&v)[N], RowSum<M> &s, const RowTe
         __syncthreads();
     else
         asm volatile("bar.sync %0, %1;" ::"r"(1 + m.rg), "r"(32 * W) : "memory");
-    if (W <= 16) {
-        const int l = lane & 15;
-        if constexpr (N == 1) {
-            v[0] = warp_total_from<8>(l < W ? s.buf[turn][0][first + l] : 0.f);
-        } else {
-            x = warp_total_from<8>(l < W ? s.buf[turn][lane >> 4][first + l] : 0.f);
-            v[0] = __shfl_sync(0xFFFFFFFFu, x, 0);
-            v[1] = __shfl_sync(0xFFFFFFFFu, x, 16);
-            if constexpr (N > 2)
-                v[2] = warp_total_from<8>(l < W ? s.buf[turn][2][first + l] : 0.f);
-        }
+    const int l = lane & 15;
+    if constexpr (N == 1) {
+        v[0] = warp_total_from<8>(l < W ? s.buf[turn][0][first + l] : 0.f);
     } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            v[i] = warp_total_from<16>(lane < W ? s.buf[turn][i][first + lane] : 0.f);
+        x = warp_total_from<8>(l < W ? s.buf[turn][lane >> 4][first + l] : 0.f);
+        v[0] = __shfl_sync(0xFFFFFFFFu, x, 0);
+        v[1] = __shfl_sync(0xFFFFFFFFu, x, 16);
+        if constexpr (N > 2)
+            v[2] = warp_total_from<8>(l < W ? s.buf[turn][2][first + l] : 0.f);
     }
     turn ^= 1;
 }

@@ -22,10 +22,6 @@
 namespace vq {
 namespace {
 
-// Where a thread's i-th chunk of a row starts, for a row over W warps.
-template <int VEC>
-__device__ __forceinline__ int chunk_at(int i, int tid, int W) { return (tid + i * 32 * W) * VEC; }
-
 // ---------------------------------------------------------------- any rows, element by element
 //
 // Rows off the 16-byte boundaries (odd widths, windows of wider arrays): a
@@ -172,7 +168,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_kernel(const NormPreA
     bool in[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        in[i] = chunk_at<8>(i, tid, W) < a.H;
+        in[i] = chunk_at(i, tid, W) < a.H;
     long ahead = row0;   // the row the next copy is for
     auto fetch = [&](int s) {
         if (ahead < a.T) {
@@ -193,7 +189,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_kernel(const NormPreA
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (in[i])
-            load_weight(a.n.weight, a.n.dtype, a.n.offset, chunk_at<8>(i, tid, W), w[i]);
+            load_weight(a.n.weight, a.n.dtype, a.n.offset, chunk_at(i, tid, W), w[i]);
     int turn = 0, s = 0;
     for (long row = row0; row < a.T; row += stride) {
         if (S == 1) {
@@ -252,7 +248,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_kernel(const NormPos
     bool in[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        in[i] = chunk_at<8>(i, tid, W) < a.H;
+        in[i] = chunk_at(i, tid, W) < a.H;
     long ahead = row0;   // the row the next copy is for
     auto fetch = [&](int s) {
         if (ahead < a.T) {
@@ -284,9 +280,9 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_kernel(const NormPos
             w1[i][j] = w2[i][j] = splat(1.f);
         if (in[i]) {
             if (post)
-                load_weight(a.post.weight, a.post.dtype, a.post.offset, chunk_at<8>(i, tid, W), w1[i]);
+                load_weight(a.post.weight, a.post.dtype, a.post.offset, chunk_at(i, tid, W), w1[i]);
             if (next)
-                load_weight(a.next.weight, a.next.dtype, a.next.offset, chunk_at<8>(i, tid, W), w2[i]);
+                load_weight(a.next.weight, a.next.dtype, a.next.offset, chunk_at(i, tid, W), w2[i]);
         }
     }
     int turn = 0, s = 0;
@@ -368,12 +364,6 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_kernel(const NormPos
 
 constexpr int PRE_REGS[4] = {48, 64, 80, 104}, POST_REGS[4] = {64, 88, 112, 128};
 
-template <auto K, typename Args>
-cudaError_t rows(const NormShape &sh, cudaStream_t s, const Args &a)
-{
-    return launch_smem<K, NORM_SMEM>(dim3(sh.ctas), dim3(32 * sh.W * sh.R), sh.smem, s, a, sh.S);
-}
-
 template <typename HT>
 cudaError_t pre_launch(NormPreArgs a, bool vec8, cudaStream_t s)
 {
@@ -381,10 +371,10 @@ cudaError_t pre_launch(NormPreArgs a, bool vec8, cudaStream_t s)
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         switch (sh.nv) {
-        case 1: return rows<vq_norm_pre_kernel<HT, 1>>(sh, s, a);
-        case 2: return rows<vq_norm_pre_kernel<HT, 2>>(sh, s, a);
-        case 3: return rows<vq_norm_pre_kernel<HT, 3>>(sh, s, a);
-        default: return rows<vq_norm_pre_kernel<HT, 4>>(sh, s, a);
+        case 1: return launch_rows<vq_norm_pre_kernel<HT, 1>>(sh, s, a);
+        case 2: return launch_rows<vq_norm_pre_kernel<HT, 2>>(sh, s, a);
+        case 3: return launch_rows<vq_norm_pre_kernel<HT, 3>>(sh, s, a);
+        default: return launch_rows<vq_norm_pre_kernel<HT, 4>>(sh, s, a);
         }
     }
     const NormShape sc = scalar_shape(a.H, a.T, 1, 0);
@@ -400,10 +390,10 @@ cudaError_t post_launch(NormPostArgs a, bool vec8, cudaStream_t s)
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         switch (sh.nv) {
-        case 1: return rows<vq_norm_post_kernel<YT, HT, 1>>(sh, s, a);
-        case 2: return rows<vq_norm_post_kernel<YT, HT, 2>>(sh, s, a);
-        case 3: return rows<vq_norm_post_kernel<YT, HT, 3>>(sh, s, a);
-        default: return rows<vq_norm_post_kernel<YT, HT, 4>>(sh, s, a);
+        case 1: return launch_rows<vq_norm_post_kernel<YT, HT, 1>>(sh, s, a);
+        case 2: return launch_rows<vq_norm_post_kernel<YT, HT, 2>>(sh, s, a);
+        case 3: return launch_rows<vq_norm_post_kernel<YT, HT, 3>>(sh, s, a);
+        default: return launch_rows<vq_norm_post_kernel<YT, HT, 4>>(sh, s, a);
         }
     }
     const NormShape sc = scalar_shape(a.H, a.T, 1, 0);

@@ -6,6 +6,9 @@
 #include <stdint.h>
 
 #include "vq_internal.h"
+#ifdef __CUDACC__
+#include "vq_block.cuh"
+#endif
 
 namespace vq {
 
@@ -124,12 +127,23 @@ struct NormShape {
     int W, R, nv, S, ctas;
     size_t smem;
 };
-constexpr int ROW_THREADS = 512;           // most threads a row
 constexpr int NORM_SMEM = 222 * 1024;      // shared memory of an SM given to the rings
 // bytes: of input an element copied ahead; fixed: bytes an element kept for the whole launch; regs: registers a
 // thread at nv chunks (regs[nv - 1]); nv, max_nv: chunks a thread takes when rows stream, and the most it has
 // registers for; max_ctas: 0, or the most CTAs.
 NormShape norm_shape(int H, int T, int bytes, int fixed, const int (&regs)[4], int nv, int max_nv, int max_ctas);
+
+#ifdef __CUDACC__
+// Where a thread's i-th chunk of a row starts, for a row over W warps.
+__device__ __forceinline__ int chunk_at(int i, int tid, int W) { return (tid + i * 32 * W) * 8; }
+
+// Launches a ring kernel over the shape's rows.
+template <auto K, typename Args>
+cudaError_t launch_rows(const NormShape &sh, cudaStream_t s, const Args &a)
+{
+    return launch_smem<K, NORM_SMEM>(dim3(sh.ctas), dim3(32 * sh.W * sh.R), sh.smem, s, a, sh.S);
+}
+#endif
 
 // The same for the element-by-element kernels: about 256 threads a CTA, `floats` fp32 values an element in shared
 // memory for each of its rows side by side.

@@ -26,9 +26,6 @@ namespace {
 
 constexpr int NORM_PARTS = 592;     // most partial rows: 4 CTAs on each of 148 SMs
 
-template <int VEC>
-__device__ __forceinline__ int chunk_at(int i, int tid, int W) { return (tid + i * 32 * W) * VEC; }
-
 // ---------------------------------------------------------------- any rows, element by element
 //
 // A thread's columns are the same in every row, so the weight gradients' sums
@@ -241,19 +238,19 @@ __device__ __forceinline__ void write_part(float *part, float2 (&acc)[NV][4], fl
         if (rg == r)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (chunk_at<8>(i, tid, W) < H) {
+                if (chunk_at(i, tid, W) < H) {
                     Chunk<float, 8> o;
                     o.set(acc[i]);
-                    o.store(side + chunk_at<8>(i, tid, W));
+                    o.store(side + chunk_at(i, tid, W));
                 }
         __syncthreads();
         if (rg == 0)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (chunk_at<8>(i, tid, W) < H) {
+                if (chunk_at(i, tid, W) < H) {
                     Chunk<float, 8> o;
                     float2 v[4];
-                    o.load(side + chunk_at<8>(i, tid, W));
+                    o.load(side + chunk_at(i, tid, W));
                     o.get(v);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -263,7 +260,7 @@ __device__ __forceinline__ void write_part(float *part, float2 (&acc)[NV][4], fl
     if (rg == 0)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = chunk_at<8>(i, tid, W);
+            const int c = chunk_at(i, tid, W);
             if (c < H) {
                 Chunk<float, 8> o;
                 o.set(acc[i]);
@@ -292,7 +289,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_bwd_kernel(const Norm
     bool in[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        in[i] = chunk_at<8>(i, tid, W) < a.H;
+        in[i] = chunk_at(i, tid, W) < a.H;
     long ahead = row0;   // the row the next copy is for
     auto fetch = [&](int s) {
         if (ahead < a.T) {
@@ -320,7 +317,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_bwd_kernel(const Norm
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         if (in[i])
-            load_weight(a.n.weight, a.n.dtype, a.n.offset, chunk_at<8>(i, tid, W), w[i]);
+            load_weight(a.n.weight, a.n.dtype, a.n.offset, chunk_at(i, tid, W), w[i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             acc[i][j] = splat(0.f);
@@ -411,7 +408,7 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
     bool in[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        in[i] = chunk_at<8>(i, tid, W) < a.H;
+        in[i] = chunk_at(i, tid, W) < a.H;
     long ahead = row0;   // the row the next copy is for
     auto fetch = [&](int s) {
         if (ahead < a.T) {
@@ -444,9 +441,9 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_bwd_kernel(const Nor
 #pragma unroll
     for (int i = 0; i < NV; ++i) {   // the weights come with the first row's copies
         if (in[i] && post)
-            ring_copy_any(at1 + p1 * i * wstep, wstep, a.post.weight, a.post.dtype, chunk_at<8>(i, tid, W));
+            ring_copy_any(at1 + p1 * i * wstep, wstep, a.post.weight, a.post.dtype, chunk_at(i, tid, W));
         if (in[i] && next)
-            ring_copy_any(at2 + p2 * i * wstep, wstep, a.next.weight, a.next.dtype, chunk_at<8>(i, tid, W));
+            ring_copy_any(at2 + p2 * i * wstep, wstep, a.next.weight, a.next.dtype, chunk_at(i, tid, W));
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             acc1[i][j] = acc2[i][j] = splat(0.f);
@@ -653,12 +650,6 @@ cudaError_t finish(int parts, int H, const float *p1, float *d1, const float *p2
 
 constexpr int PRE_BWD_REGS[4] = {64, 88, 112, 128}, POST_BWD_REGS[4] = {96, 128, 128, 128};
 
-template <auto K, typename Args>
-cudaError_t rows(const NormShape &sh, cudaStream_t s, const Args &a)
-{
-    return launch_smem<K, NORM_SMEM>(dim3(sh.ctas), dim3(32 * sh.W * sh.R), sh.smem, s, a, sh.S);
-}
-
 // Both launch and say how many partial rows they leave.
 template <typename HT>
 cudaError_t pre_bwd(NormPreBwdArgs a, bool vec8, int &parts, cudaStream_t s)
@@ -668,10 +659,10 @@ cudaError_t pre_bwd(NormPreBwdArgs a, bool vec8, int &parts, cudaStream_t s)
         a.W = sh.W;
         parts = sh.ctas;
         switch (sh.nv) {
-        case 1: return rows<vq_norm_pre_bwd_kernel<HT, 1>>(sh, s, a);
-        case 2: return rows<vq_norm_pre_bwd_kernel<HT, 2>>(sh, s, a);
-        case 3: return rows<vq_norm_pre_bwd_kernel<HT, 3>>(sh, s, a);
-        default: return rows<vq_norm_pre_bwd_kernel<HT, 4>>(sh, s, a);
+        case 1: return launch_rows<vq_norm_pre_bwd_kernel<HT, 1>>(sh, s, a);
+        case 2: return launch_rows<vq_norm_pre_bwd_kernel<HT, 2>>(sh, s, a);
+        case 3: return launch_rows<vq_norm_pre_bwd_kernel<HT, 3>>(sh, s, a);
+        default: return launch_rows<vq_norm_pre_bwd_kernel<HT, 4>>(sh, s, a);
         }
     }
     sh = scalar_shape(a.H, a.T, 1, NORM_PARTS);
@@ -691,10 +682,10 @@ cudaError_t post_bwd(NormPostBwdArgs a, bool vec8, int &parts, cudaStream_t s)
         a.W = sh.W;
         parts = sh.ctas;
         switch (sh.nv) {
-        case 1: return rows<vq_norm_post_bwd_kernel<YT, HT, 1>>(sh, s, a);
-        case 2: return rows<vq_norm_post_bwd_kernel<YT, HT, 2>>(sh, s, a);
-        case 3: return rows<vq_norm_post_bwd_kernel<YT, HT, 3>>(sh, s, a);
-        default: return rows<vq_norm_post_bwd_kernel<YT, HT, 4>>(sh, s, a);
+        case 1: return launch_rows<vq_norm_post_bwd_kernel<YT, HT, 1>>(sh, s, a);
+        case 2: return launch_rows<vq_norm_post_bwd_kernel<YT, HT, 2>>(sh, s, a);
+        case 3: return launch_rows<vq_norm_post_bwd_kernel<YT, HT, 3>>(sh, s, a);
+        default: return launch_rows<vq_norm_post_bwd_kernel<YT, HT, 4>>(sh, s, a);
         }
     }
     sh = scalar_shape(a.H, a.T, 3, NORM_PARTS);
