@@ -1,4 +1,8 @@
 """The block operators with weights and arrays that change between calls."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -69,3 +73,33 @@ def test_x_rewritten_by_the_call_before_the_experts(T, path, writer):
         got.append((y, vq.q4_gemv(m, x)))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for p, q in zip(got, want) for a, b in zip(p, q))
+
+
+FIRST_CALLS = """
+import torch
+import vector_quantized_moe_b200 as vq
+T, H = 700, 256
+g = torch.Generator().manual_seed(1)
+h, y = torch.randn((T, H), generator=g).cuda(), torch.randn((T, H), generator=g).cuda()
+d = torch.randn((T, H), generator=g).bfloat16().cuda()
+n = vq.Norm(torch.ones(H, device="cuda"))
+def run():
+    ho, x = vq.norm_post(y, h, n, next=n)
+    return (vq.norm_pre(n, h), ho, x, *vq.norm_pre_backward(n, h, d), *vq.norm_post_backward(y, ho, h, d, n, next=n))
+torch.zeros(1, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(a is b or torch.equal(a, b) for a, b in zip(got, run()))
+print("equal")
+"""
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    # what the launches ask the runtime once (registers, shared memory) is allowed during a capture
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "equal", r.stderr[-2000:]

@@ -362,12 +362,15 @@ __global__ void __launch_bounds__(ROW_THREADS) vq_norm_post_kernel(const NormPos
     }
 }
 
-constexpr int PRE_REGS[4] = {48, 64, 80, 104}, POST_REGS[4] = {64, 88, 112, 128};
-
 template <typename HT>
 cudaError_t pre_launch(NormPreArgs a, bool vec8, cudaStream_t s)
 {
-    const NormShape sh = norm_shape(a.H, a.T, sizeof(HT), 0, PRE_REGS, 2, 2, 0);
+    int regs[4];
+    const cudaError_t e = ring_regs<vq_norm_pre_kernel<HT, 1>, vq_norm_pre_kernel<HT, 2>, vq_norm_pre_kernel<HT, 3>,
+                                    vq_norm_pre_kernel<HT, 4>>(regs);
+    if (e != cudaSuccess)
+        return e;
+    const NormShape sh = norm_shape(a.H, a.T, sizeof(HT), 0, regs, 2, 2, 0);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         switch (sh.nv) {
@@ -386,7 +389,12 @@ template <typename YT, typename HT>
 cudaError_t post_launch(NormPostArgs a, bool vec8, cudaStream_t s)
 {
     const int gate = a.gate_mode != GATE_CHANNEL ? 0 : a.gate_dtype == VQ_F32 ? 4 : 2;
-    const NormShape sh = norm_shape(a.H, a.T, sizeof(YT) + sizeof(HT) + gate, 0, POST_REGS, 2, 3, 0);
+    int regs[4];
+    const cudaError_t e = ring_regs<vq_norm_post_kernel<YT, HT, 1>, vq_norm_post_kernel<YT, HT, 2>,
+                                    vq_norm_post_kernel<YT, HT, 3>, vq_norm_post_kernel<YT, HT, 4>>(regs);
+    if (e != cudaSuccess)
+        return e;
+    const NormShape sh = norm_shape(a.H, a.T, sizeof(YT) + sizeof(HT) + gate, 0, regs, 2, 3, 0);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         switch (sh.nv) {

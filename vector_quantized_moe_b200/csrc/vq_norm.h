@@ -129,13 +129,33 @@ struct NormShape {
 };
 constexpr int NORM_SMEM = 222 * 1024;      // shared memory of an SM given to the rings
 // bytes: of input an element copied ahead; fixed: bytes an element kept for the whole launch; regs: registers a
-// thread at nv chunks (regs[nv - 1]); nv, max_nv: chunks a thread takes when rows stream, and the most it has
+// thread of the kernel with nv chunks (regs[nv - 1]), which bound the CTAs that an SM holds; nv, max_nv: chunks a thread takes when rows stream, and the most it has
 // registers for; max_ctas: 0, or the most CTAs.
 NormShape norm_shape(int H, int T, int bytes, int fixed, const int (&regs)[4], int nv, int max_nv, int max_ctas);
 
 #ifdef __CUDACC__
 // Where a thread's i-th chunk of a row starts, for a row over W warps.
 __device__ __forceinline__ int chunk_at(int i, int tid, int W) { return (tid + i * 32 * W) * 8; }
+
+// Registers a thread of the kernels with 1 to 4 chunks, as allocated (in units of 8), asked for once.
+template <auto K1, auto K2, auto K3, auto K4>
+cudaError_t ring_regs(int (&regs)[4])
+{
+    static std::atomic<int> known[4];
+    const void *kernels[4] = {(const void *)K1, (const void *)K2, (const void *)K3, (const void *)K4};
+    for (int i = 0; i < 4; ++i) {
+        regs[i] = known[i].load(std::memory_order_relaxed);
+        if (regs[i] == 0) {
+            cudaFuncAttributes f;
+            const cudaError_t e = cudaFuncGetAttributes(&f, kernels[i]);
+            if (e != cudaSuccess)
+                return e;
+            regs[i] = (f.numRegs + 7) / 8 * 8;
+            known[i].store(regs[i], std::memory_order_relaxed);
+        }
+    }
+    return cudaSuccess;
+}
 
 // Launches a ring kernel over the shape's rows.
 template <auto K, typename Args>

@@ -648,13 +648,16 @@ cudaError_t finish(int parts, int H, const float *p1, float *d1, const float *p2
     return launch_after(vq_norm_dw_kernel, dim3((H + 31) / 32, d2 ? 2 : 1), dim3(1024), 0, s, p1, d1, p2, d2, parts, H);
 }
 
-constexpr int PRE_BWD_REGS[4] = {64, 88, 112, 128}, POST_BWD_REGS[4] = {96, 128, 128, 128};
-
 // Both launch and say how many partial rows they leave.
 template <typename HT>
 cudaError_t pre_bwd(NormPreBwdArgs a, bool vec8, int &parts, cudaStream_t s)
 {
-    NormShape sh = norm_shape(a.H, a.T, sizeof(HT) * (a.dres ? 2 : 1) + 2, 0, PRE_BWD_REGS, 4, 4, NORM_PARTS);
+    int regs[4];
+    const cudaError_t e = ring_regs<vq_norm_pre_bwd_kernel<HT, 1>, vq_norm_pre_bwd_kernel<HT, 2>,
+                                    vq_norm_pre_bwd_kernel<HT, 3>, vq_norm_pre_bwd_kernel<HT, 4>>(regs);
+    if (e != cudaSuccess)
+        return e;
+    NormShape sh = norm_shape(a.H, a.T, sizeof(HT) * (a.dres ? 2 : 1) + 2, 0, regs, 4, 4, NORM_PARTS);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         parts = sh.ctas;
@@ -676,8 +679,13 @@ cudaError_t post_bwd(NormPostBwdArgs a, bool vec8, int &parts, cudaStream_t s)
 {
     const int gate = a.gate_mode != GATE_CHANNEL ? 0 : a.gate_dtype == VQ_F32 ? 4 : 2;
     auto w = [](const NormDev &n) { return !n.weight ? 0 : n.dtype == VQ_F32 ? 4 : 2; };
+    int regs[4];
+    const cudaError_t e = ring_regs<vq_norm_post_bwd_kernel<YT, HT, 1>, vq_norm_post_bwd_kernel<YT, HT, 2>,
+                                    vq_norm_post_bwd_kernel<YT, HT, 3>, vq_norm_post_bwd_kernel<YT, HT, 4>>(regs);
+    if (e != cudaSuccess)
+        return e;
     NormShape sh = norm_shape(a.H, a.T, sizeof(YT) + (a.dho ? sizeof(HT) : 0) + (a.next.weight ? sizeof(HT) + 2 : 0) + gate,
-                              w(a.post) + w(a.next), POST_BWD_REGS, 2, 2, NORM_PARTS);
+                              w(a.post) + w(a.next), regs, 2, 2, NORM_PARTS);
     if (vec8 && sh.S > 0) {
         a.W = sh.W;
         parts = sh.ctas;
