@@ -8,6 +8,7 @@ import torch
 
 import vector_quantized_moe_b200 as vq
 from helpers import lib_module, small_module
+from test_gpu_block import make
 from test_gpu_q4 import module, tokens
 
 pytestmark = pytest.mark.gpu
@@ -103,3 +104,41 @@ def test_the_first_calls_of_a_process_can_be_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "equal", r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("path", ["decode", "prefill"])
+def test_blocks_of_unusual_rows(path):
+    # no rows, windows of wider rows, bit patterns of bf16, another stream: the same bits as plain rows give
+    block, _, _ = make(True, True, True)
+    run = getattr(block, path)
+    H = block.layer.hidden
+    for T in (0, 1, 7):
+        h = torch.randn((T, H), generator=torch.Generator().manual_seed(50 + T)).bfloat16().cuda()
+        want = run(h)
+        assert want[0].shape == want[1].shape == (T, H) and want[2].shape == (T, block.layer.E)
+        wide = torch.full((T + 1, H + 24), 9.0, dtype=torch.bfloat16, device="cuda")
+        wide[:T, 8:8 + H] = h
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            other = run(h)
+        s.synchronize()
+        for got in (run(wide[:T, 8:8 + H]), run(h.view(torch.int16)), run(h, vq.norm_pre(block.pre, h)), other):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_gates_of_any_stride():
+    T, H = 5, 256
+    g = torch.Generator().manual_seed(60)
+    y, h = torch.randn((T, H), generator=g).cuda(), torch.randn((T, H), generator=g).cuda()
+    z = torch.randn((T, 9), generator=g).cuda()
+    want = vq.norm_post(y, h, gate=z[:, 3].contiguous())[0]
+    back = vq.norm_post_backward(y, want, h, gate=z[:, 3].contiguous())
+    assert back[1].shape == (T,)
+    for gate in (z[:, 3], z[:, 3:4], z.T.contiguous().T[:, 3], z[:, 3].contiguous()[:, None]):
+        assert torch.equal(vq.norm_post(y, h, gate=gate)[0], want)
+        got = vq.norm_post_backward(y, want, h, gate=gate)
+        assert got[1].shape == gate.shape and got[1].is_contiguous()
+        assert torch.equal(got[1].reshape(T), back[1]) and torch.equal(got[0], back[0])
+    flipped = z.flip(0)[:, 3]
+    assert torch.equal(vq.norm_post(y, h, gate=flipped)[0], vq.norm_post(y, h, gate=flipped.contiguous())[0])
