@@ -436,8 +436,10 @@ vq_status vq_q4_pack(const uint32_t *codes, const uint16_t *scales, const uint16
  * elements, 16-byte aligned, x_ld a multiple of 8 (T > 1). y: device [T, rows] of y_dtype, row stride y_ld >= rows,
  * aligned to its element. x enters the tensor cores unrounded as bf16 against the exact integers 16 + q; group sums
  * (24 sum x is taken off them), scales and the sum over groups are fp32 in a fixed order, and y is rounded once: the
- * error is a few 2^-24 of sum |scale| (16 + q) |x|. Sums of (16 + q) |x| over a group have to stay in fp32's range. The
- * weights are streamed once for every 16 tokens: the call is meant for decode-sized T (T > 16 * 65535: VQ_ERR_UNSUPPORTED). An
+ * error is a few 2^-24 of sum |scale| (16 + q) |x|, also where the weights' own sum is much smaller (a row of codes 8
+ * is 0 within it, not exactly). Sums of (16 + q) |x| over a group have to stay in fp32's range. The
+ * weights are streamed and decoded once for every 16 tokens, so that the time grows with T from there on: the call is
+ * meant for decode-sized T (T > 16 * 65535: VQ_ERR_UNSUPPORTED). An
  * Inf or NaN in x gives Inf or NaN in its token's outputs. */
 vq_status vq_q4_gemv(const vq_q4_module *m0, const vq_q4_module *m1, const uint16_t *x, int64_t x_ld, int32_t T,
                      void *y, int32_t y_dtype, int64_t y_ld, void *stream);

@@ -11,10 +11,10 @@
 // its tokens in registers. Few tokens: one CTA does it all. More: CTAs write
 // partial sums and counts, and one cluster of CTAs adds them in order.
 //
-// Measured: 32768 x 512, loss 18 us + 5 us for the partial rows, gradient 23 us, 45.7 us
+// Measured: 32768 x 512, loss 18 us + 5 us for the partial rows, gradient 23 us, 45.2 us
 // together; reading the logits twice and writing the gradient is 31 us at the
-// copy rate. 4096 x 256 12.0 us and 16 x 512 5.9 us, both of them the launches. With the next row
-// loaded ahead and the pairs counted on the way 45.7 us, without 68.
+// copy rate. 4096 x 256 12.1 us and 16 x 512 5.9 us, both of them the launches. With the next row
+// loaded ahead and the pairs counted on the way 45.2 us, without 68.
 #include <algorithm>
 
 #include "vq_block.cuh"

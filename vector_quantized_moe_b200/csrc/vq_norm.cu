@@ -7,13 +7,17 @@
 //
 // A row stays in the registers of one CTA (or one warp) between the row sum
 // and the output, so each array crosses HBM once. Many rows: persistent CTAs
-// with the next rows on their way. 4096 x 4096 bf16 with both norms takes 27.8
-// us for 134 MB (4.8 TB/s, 0.74 of the copy rate), 4096 x 6144 35.8 us (0.86), 16384 x
-// 512 13.9 us (0.74); a CTA per row from registers took 43 us for the first.
+// with the next rows on their way. 4096 x 4096 bf16 with both norms takes 27.3
+// us for 134 MB (4.9 TB/s, 0.75 of the copy rate), 4096 x 6144 36.5 us (0.84), 16384 x
+// 512 13.9 us (0.74); a CTA per row from registers took 43 us for the first. norm_pre 4096
+// x 4096 takes 12.9 us (0.80), 65536 x 256 12.6 us (0.82).
 // What is left is latency: two row sums per row with 16 to 24 warps on an SM,
-// which issue 2.1 instructions a cycle between them. Few rows: one load, one or two row sums
-// and one store, 1.8 us (1 x 4096, pre) to 4.1 us (16 x 6144, post), the launch
-// included.
+// which issue 2.1 instructions a cycle between them. The warps are as many as registers
+// allow: both weights of a thread's columns stay in them as fp32 (32 of 89 to 120 with two
+// chunks). Weights in shared memory, as the gradient has them, were not tried here. With
+// four chunks (hidden over 12288) norm_post spills 60 to 110 bytes a thread: 1024 x 16384
+// 49 us (0.53). Few rows: one load, one or two row sums and one store, 1.9 us (1 x 4096, pre)
+// to 4.1 us (16 x 6144, post), the launch included.
 #include <algorithm>
 
 #include "vq_block.cuh"
@@ -26,7 +30,9 @@ namespace {
 //
 // Rows off the 16-byte boundaries (odd widths, windows of wider arrays): a
 // warp's loads and stores are contiguous elements, a row's fp32 values wait in
-// shared memory between the passes, and several CTAs on an SM overlap.
+// shared memory between the passes, and several CTAs on an SM overlap. 1024 x 4099:
+// norm_pre 11.4 us, norm_post (fp32 y) 26.7 us, where the bytes take 2.6 and 6.4: an access
+// moves 2 or 4 bytes a lane, and nothing of a CTA's next row is on its way while it works on one.
 
 template <typename HT>
 __global__ void __launch_bounds__(ROW_THREADS) vq_norm_pre_scalar_kernel(const NormPreArgs a)

@@ -10,12 +10,14 @@
 // statistics are saved: the row sums that need only the inputs (|h'|^2, g h',
 // |y|^2) come out of one pass, so recomputing them adds no barrier.
 //
-// Measured: norm_pre's 4096 x 6144 bf16 with a residual gradient 38.2 us for 201 MB
+// Measured: norm_pre's 4096 x 6144 bf16 with a residual gradient 37.9 us for 201 MB
 // (5.3 TB/s, 0.81 of the copy rate); norm_post's 2047 x 4096 with both norms and a
-// gate per channel 48.5 us for 168 MB (3.5 TB/s, 0.53). The second holds 128 registers a
+// gate per channel 47.6 us for 168 MB (3.5 TB/s, 0.54). The second holds 128 registers a
 // thread (two weight gradients), so an SM has 16 warps, at two rows a time; it
 // is bound by their latency between the two row sums (1.8 instructions a
-// cycle), not by HBM.
+// cycle), not by HBM. Wider rows have one CTA of one row on an SM, 12 warps at
+// 6144: 4096 x 6144 (fp32 y) 121 us (0.51). With three and four chunks (hidden over 8192) it
+// spills 130 to 660 bytes a thread: 1024 x 12288 83 us (0.37), 1024 x 16384 306 us (0.13).
 #include <algorithm>
 
 #include "vq_block.cuh"
@@ -30,7 +32,8 @@ constexpr int NORM_PARTS = 592;     // most partial rows: 4 CTAs on each of 148 
 //
 // A thread's columns are the same in every row, so the weight gradients' sums
 // wait in shared memory without a barrier. Arrays are read again in each pass
-// (from L1 or L2).
+// (from L1 or L2), 2 or 4 bytes a lane. 1024 x 4099: norm_pre's 32 us, norm_post's (fp32 y)
+// 77 us, where the bytes take 5.1 and 10.3.
 
 // A CTA's partial row: its side-by-side rows' sums (the first floats of each row's share) added in order.
 __device__ __forceinline__ void write_part_scalar(float *part, const float *acc, int share, int R, int H)

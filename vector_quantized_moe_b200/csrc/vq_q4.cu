@@ -9,9 +9,9 @@
 // weights and no subtraction. 24 times a group's sum of x comes off its sum in
 // fp32; the sum of x comes out of the same instruction against ones, in the
 // lanes that need it. The offset makes the sums of a group about 5 times
-// larger than those of q - 8, so their fp32 rounding counts that much more
-// (131072 x 4096, against 64 bits: 1.3e-7 of the result's norm; a plain fp32
-// product 3.3e-7).
+// larger than those of q - 8, so their fp32 rounding counts that much more. Against 64
+// bits, relative to the result's norm: 131072 x 4096, tokens of mean 0, 2.1e-7 (a plain fp32
+// product 3.3e-7); tokens with a common offset of 1 to 100, 2e-7 to 7e-7 (plain: 4e-8 to 1.1e-7).
 //
 // The weights dominate the bytes (0.5 byte each, read once), so the layout is
 // the lanes' own: one 16-byte load per lane is four mma A operands of a 16 x 64
@@ -21,14 +21,16 @@
 // fragments serve R tiles; the CTA's warps take column tiles in turn and add
 // their sums through shared memory in warp order.
 //
-// Measured (GPU time): 131072 x 4096, 8 tokens 53.3 us for 281 MB (5.3 TB/s, 0.81 of the
+// Measured (GPU time): 131072 x 4096, 8 tokens 53.1 us for 281 MB (5.3 TB/s, 0.81 of the
 // copy rate; the copies alone, without decoding and mma, take 45 us); bound by
 // the ALU pipe (65% busy: three shifts and four mask-ors per word, 7 per 8
-// weights, at half rate) and the latency of 16 warps on an SM. 6144 x 6144, 1 token 8.3
-// us for 21 MB, 2 x 2040 x 6144, 16 tokens 8.7 us: 3 to 6 turns of a warp at 0.9 to 1.2 us and
+// weights, at half rate) and the latency of 16 warps on an SM. 6144 x 6144, 1 token 8.4
+// us for 21 MB, 2 x 2040 x 6144, 16 tokens 9.0 us: 3 to 6 turns of a warp at 0.9 to 1.2 us and
 // 2 to 4 us of start and end. The subtraction of 8 as an instruction: 171
 // instructions a 16 x 128 tile instead of 126. Shifts as high multiplies on
 // the FMA pipe: 73 us. Persistent CTAs that copy ahead across row groups: 64 us.
+// Every 16 tokens more decode all weights once more: 16384 x 4096, 16 tokens 17.6 us, 32
+// tokens 30.2 us.
 #include <algorithm>
 
 #include "vq_block.cuh"
