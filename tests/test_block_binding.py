@@ -1,6 +1,6 @@
 """What the block operators' binding hands to the library, and what it refuses before it does: weights and modules as
 they are at the call. CPU tensors throughout; the library's launch is replaced by a record of its arguments."""
-import ctypes
+import copy
 
 import pytest
 import torch
@@ -211,3 +211,28 @@ def test_a_layer_knows_the_one_device_of_its_arrays():
         setattr(mods[2], name, OnGPU(old))
         assert vq.MoELayer(*mods)._dev is None
         setattr(mods[2], name, old)
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy])
+def test_copies_are_bound_for_themselves(launches, how):
+    v = torch.zeros((2, 64), dtype=BF16)
+    n = vq.Norm(torch.ones(64), 1e-5, 1.0)
+    n.name = "input"
+    vq.norm_pre(n, v)
+    c = how(n)
+    assert c.name == "input" and c.hidden == 64
+    c.weight = torch.full((64,), 2.0)
+    launches.clear()
+    for each in (c, n, c):
+        vq.norm_pre(each, v)
+        s = struct(launches[-1][1][0])
+        assert s.weight == address(each.weight) and s.weight_offset == 1.0 and abs(s.eps - 1e-5) < 1e-12
+    m = vq.Q4Module(64, 128, 64, *q4_arrays(64, 128, 64, True))
+    x = torch.zeros((2, 128), dtype=BF16)
+    vq.q4_gemv(m, x)
+    c = how(m)
+    c.scales = m.scales.clone()
+    for each in (c, m, c):
+        vq.q4_gemv(each, x)
+        s = struct(launches[-1][1][0])
+        assert (s.words, s.scales, s.biases) == (address(each.words), address(each.scales), address(each.biases))

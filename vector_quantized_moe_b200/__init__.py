@@ -421,6 +421,10 @@ def _one_device(where, first, *others) -> int:
     return dev
 
 
+def _public(o):
+    return {k: v for k, v in vars(o).items() if k[0] != "_"}
+
+
 class Norm:
     """The weight of a root-mean-square norm (vq_norm): weight [hidden] fp32 or bf16; offset is 1 for checkpoints that
     store weight - 1. A call uses the weight as it is then: another one may be assigned, or new data to it."""
@@ -456,6 +460,9 @@ class Norm:
             self._at = None
             self._bind()
         return self._ref
+
+    def __reduce__(self):   # a copy has a struct of its own
+        return type(self), (self.weight, self._s.eps, self._s.weight_offset), _public(self)
 
     def _held(self):
         return [self.weight]
@@ -736,6 +743,9 @@ class Q4Module:
         s = self._s
         s.rows, s.cols, s.group = rows, cols, group
         s.words, s.scales, s.biases = _ptr(self.words), _ptr(self.scales), _ptr(self.biases)
+
+    def __reduce__(self):   # a copy has a struct of its own
+        return (type(self), (self.rows, self.cols, self.group, self.words, self.scales, self.biases), _public(self))
 
     def _held(self):
         return [self.words, self.scales, self.biases]
