@@ -1,6 +1,7 @@
 """What the block operators' binding hands to the library, and what it refuses before it does: weights and modules as
 they are at the call. CPU tensors throughout; the library's launch is replaced by a record of its arguments."""
 import copy
+import types
 
 import pytest
 import torch
@@ -236,3 +237,10 @@ def test_copies_are_bound_for_themselves(launches, how):
         vq.q4_gemv(each, x)
         s = struct(launches[-1][1][0])
         assert (s.words, s.scales, s.biases) == (address(each.words), address(each.scales), address(each.biases))
+
+
+def test_a_block_around_a_layer_of_another_class(block):
+    plain = types.SimpleNamespace(**{k: getattr(block.layer, k) for k in ("hidden", "E", "workspace_size", "decode", "prefill")})
+    b = vq.MoEBlock(plain, block.pre, block.router, 2)
+    b.decode(torch.zeros((3, 512)))
+    assert len(block.seen) == 1

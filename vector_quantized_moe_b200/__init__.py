@@ -944,7 +944,7 @@ class MoEBlock:
         if dev != _device():
             with _torch().cuda.device(dev):
                 return self._run(experts, mode, h, x, workspace)
-        if dev != self.layer._dev:
+        if dev != getattr(self.layer, "_dev", dev):   # (a layer of the caller's own making knows its device itself)
             _bad("MoEBlock (layer on another device)")
         if h.dim() != 2 or h.shape[1] != self.layer.hidden:   # the experts read rows of hidden elements of x
             _bad("MoEBlock: h")
