@@ -129,8 +129,8 @@ struct NormShape {
 };
 constexpr int NORM_SMEM = 222 * 1024;      // shared memory of an SM given to the rings
 // bytes: of input an element copied ahead; fixed: bytes an element kept for the whole launch; regs: registers a
-// thread of the kernel with nv chunks (regs[nv - 1]), which bound the CTAs that an SM holds; nv, max_nv: chunks a thread takes when rows stream, and the most it has
-// registers for; max_ctas: 0, or the most CTAs.
+// thread of the kernel with nv chunks (regs[nv - 1]), which bound the CTAs that an SM holds; nv, max_nv: chunks a
+// thread takes when rows stream, and the most it has registers for; max_ctas: 0, or the most CTAs.
 NormShape norm_shape(int H, int T, int bytes, int fixed, const int (&regs)[4], int nv, int max_nv, int max_ctas);
 
 #ifdef __CUDACC__
